@@ -28,6 +28,7 @@ VDA_SCAN_CHUNKS = 2
 NOALLOC_SCRATCH_BYTES = 16 << 20   # VDA_NOALLOC_SCRATCH_BYTES in include/vda.h
 
 c_int, c_size_t, c_void_p, c_float = ctypes.c_int, ctypes.c_size_t, ctypes.c_void_p, ctypes.c_float
+c_int64 = ctypes.c_int64
 c_float_p = ctypes.POINTER(ctypes.c_float)
 c_int_p = ctypes.POINTER(ctypes.c_int)
 
@@ -59,6 +60,42 @@ class VdaPrepArgs(ctypes.Structure):
     ]
 
 
+class VdaRows(ctypes.Structure):
+    """Mirror of `vda_rows` in include/vda.h."""
+    _fields_ = [("data", c_void_p), ("token_stride", c_int64), ("head_stride", c_int64)]
+
+
+class VdaQkArgs(ctypes.Structure):
+    """Mirror of `vda_qk_args` in include/vda.h."""
+    _fields_ = [
+        ("dtype", c_int),
+        ("q_in", VdaRows), ("k_in", VdaRows), ("v_in", VdaRows), ("q_out", VdaRows), ("k_out", VdaRows),
+        ("q_weight", c_void_p), ("k_weight", c_void_p),
+        ("positions", c_void_p), ("frequencies", c_void_p), ("axis", c_void_p),
+        ("slots", c_void_p), ("k_cache", c_void_p), ("v_cache", c_void_p),
+        ("N", c_int), ("Hq", c_int), ("Hk", c_int), ("d", c_int),
+        ("axes", c_int), ("rot", c_int), ("interleaved", c_int),
+        ("pages", c_int), ("page_size", c_int),
+        ("eps", c_float),
+        ("stream", c_void_p),
+    ]
+
+
+class VdaQkGradArgs(ctypes.Structure):
+    """Mirror of `vda_qk_grad_args` in include/vda.h."""
+    _fields_ = [
+        ("dtype", c_int),
+        ("dq_out", VdaRows), ("dk_out", VdaRows), ("q_in", VdaRows), ("k_in", VdaRows),
+        ("dq_in", VdaRows), ("dk_in", VdaRows),
+        ("q_weight", c_void_p), ("k_weight", c_void_p), ("dq_weight", c_void_p), ("dk_weight", c_void_p),
+        ("positions", c_void_p), ("frequencies", c_void_p), ("axis", c_void_p),
+        ("N", c_int), ("Hq", c_int), ("Hk", c_int), ("d", c_int),
+        ("axes", c_int), ("rot", c_int), ("interleaved", c_int),
+        ("eps", c_float),
+        ("stream", c_void_p),
+    ]
+
+
 _SIGNATURES = {
     "vda_forward": (c_int, [c_void_p] * 8 + [c_int] * 8 + [c_void_p, c_void_p]),
     "vda_forward_f32": (c_int, [c_void_p] * 8 + [c_int] * 8 + [c_void_p, c_void_p]),
@@ -76,6 +113,9 @@ _SIGNATURES = {
     "vda_launches_per_forward": (c_int, [c_int] * 8),
     "vda_status_string": (ctypes.c_char_p, [c_int]),
     "vda_prep": (c_int, [ctypes.POINTER(VdaPrepArgs)]),
+    "vda_qk_norm_rope": (c_int, [ctypes.POINTER(VdaQkArgs)]),
+    "vda_qk_grad_workspace_bytes": (c_size_t, [c_int]),
+    "vda_qk_norm_rope_backward": (c_int, [ctypes.POINTER(VdaQkGradArgs), c_void_p, c_size_t]),
     "vda_selftest_wait_timeout": (c_int, [c_int, c_void_p]),
 }
 

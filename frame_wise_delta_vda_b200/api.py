@@ -7,12 +7,13 @@ CUDA kernels; there is no PyTorch or CPU implementation here.
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 
 import torch
 
 from ._lib import (VDA_BF16, VDA_F32, VDA_SCAN_AUTO, VDA_SCAN_CHUNKS, VDA_SCAN_FRAMES, VdaArgs,  # noqa: F401
-                   VdaError, VdaPrepArgs, check, lib)
+                   VdaError, VdaPrepArgs, VdaQkArgs, VdaQkGradArgs, VdaRows, check, lib)
 
 _SCAN_FORMS = {"auto": VDA_SCAN_AUTO, "frames": VDA_SCAN_FRAMES, "chunks": VDA_SCAN_CHUNKS}
 
@@ -169,6 +170,178 @@ def vda_prep(q_in, k_in, v_in, wk_s, wk_t, wv_s, wv_t, Hl, Wl, q_out=None, k_out
     a.stream = _stream(stream).value
     check(lib().vda_prep(ctypes.byref(a)), "vda_prep")
     return tuple(outs)
+
+
+# ---------------------------------------------------------------------------
+# Softmax branch: norm and rotation of queries and keys, paged cache, attention
+def _on_device(device):
+    """The device the library launches on, which is the current one."""
+    if device.index == torch.cuda.current_device():
+        return contextlib.nullcontext()
+    return torch.cuda.device(device)
+
+
+def _rows(name, t, dtype, shape, device):
+    """[N, heads, d] with contiguous channels, any token and head strides."""
+    if t is None:
+        raise ValueError(f"{name} is required")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
+    st = t.stride()
+    if st[2] != 1:
+        raise ValueError(f"{name} must have contiguous channels")
+    return VdaRows(t.data_ptr(), st[0], st[1])
+
+
+def rope_frequencies(rot, theta=10000.0, sections=None, device="cuda"):
+    """The (frequencies, axis) arguments of `vda_qk_norm_rope`: radians per
+    position theta ** (-2 i / c) of the i-th pair of each axis, the c = 2 *
+    pairs channels of the axes side by side.  `sections` lists the pairs of
+    each axis (default: one axis with all rot / 2)."""
+    if rot % 2:
+        raise ValueError("rot must be even")
+    sections = [rot // 2] if sections is None else list(sections)
+    if sum(sections) != rot // 2 or min(sections, default=0) < 0:
+        raise ValueError(f"sections {sections} must add up to rot / 2 = {rot // 2}")
+    freq = [theta ** (-i / c) for c in sections for i in range(c)]
+    axis = [a for a, c in enumerate(sections) for _ in range(c)]
+    return (torch.tensor(freq, dtype=torch.float64, device=device),
+            torch.tensor(axis, dtype=torch.int32, device=device))
+
+
+def _set_rotation(a, N, positions, frequencies, axis, interleaved, dev):
+    if frequencies is None:
+        if positions is not None or axis is not None:
+            raise ValueError("positions and axis need frequencies")
+        return
+    rot = 2 * frequencies.numel()
+    _check_tensor("frequencies", frequencies, torch.float64, (rot // 2,), dev)
+    if axis is not None:
+        _check_tensor("axis", axis, torch.int32, (rot // 2,), dev)
+    if positions is None or positions.dim() != 2:
+        raise ValueError("positions must be [N, axes]")
+    _check_tensor("positions", positions, torch.int32, (N, positions.shape[1]), dev)
+    if axis is None:
+        raise ValueError("axis is required with frequencies")
+    a.axes, a.rot, a.interleaved = positions.shape[1], rot, int(bool(interleaved))
+    if rot:
+        a.positions, a.frequencies, a.axis = positions.data_ptr(), frequencies.data_ptr(), axis.data_ptr()
+
+
+def _set_weight(name, w, d, dev):
+    if w is None:
+        return None
+    _check_tensor(name, w, torch.float32, (d,), dev)
+    return w.data_ptr()
+
+
+def _qk_shapes(q, k):
+    if q.dim() != 3 or k.dim() != 3:
+        raise ValueError("q and k must be [N, heads, d]")
+    N, Hq, d = q.shape
+    dt = _DTYPES.get(q.dtype)
+    if dt is None:
+        raise ValueError(f"unsupported dtype {q.dtype} (bf16 or float32)")
+    return N, Hq, k.shape[1], d, dt
+
+
+def _check_cache(k_cache, v_cache, dtype, Hk, d, dev):
+    """[pages, Hk, page_size, d], contiguous: (pages, page_size)."""
+    if k_cache is None or v_cache is None or k_cache.dim() != 4:
+        raise ValueError("k_cache and v_cache must be [pages, Hk, page_size, d]")
+    pages, _, page, _ = k_cache.shape
+    _check_tensor("k_cache", k_cache, dtype, (pages, Hk, page, d), dev)
+    _check_tensor("v_cache", v_cache, dtype, (pages, Hk, page, d), dev)
+    return pages, page
+
+
+def vda_qk_norm_rope(q, k, q_weight=None, k_weight=None, positions=None, frequencies=None, axis=None,
+                     interleaved=False, eps=1e-6, v=None, k_cache=None, v_cache=None, slots=None, q_out=None,
+                     k_out=None, stream=None):
+    """RMS norm of each head of q [N, Hq, d] and k [N, Hk, d] (weights [d]
+    float32) and the rotation of its first 2 * len(frequencies) channels by
+    positions [N, axes] int32 (see include/vda.h and `rope_frequencies`).
+    q, k and v may be strided over tokens and heads (slices of a joint
+    projection).  With `slots` [N] int64, k's result and v [N, Hk, d] go to
+    those places of k_cache and v_cache [pages, Hk, page_size, d] (slot = page
+    * page_size + offset; -1: not stored).  Returns (q_out, k_out); k_out is
+    None when only the cache receives k."""
+    N, Hq, Hk, d, dt = _qk_shapes(q, k)
+    dev = q.device
+    a = VdaQkArgs()
+    a.dtype = dt
+    a.q_in = _rows("q", q, q.dtype, (N, Hq, d), dev)
+    a.k_in = _rows("k", k, q.dtype, (N, Hk, d), dev)
+    a.N, a.Hq, a.Hk, a.d = N, Hq, Hk, d
+    a.q_weight = _set_weight("q_weight", q_weight, d, dev)
+    a.k_weight = _set_weight("k_weight", k_weight, d, dev)
+    _set_rotation(a, N, positions, frequencies, axis, interleaved, dev)
+    if slots is not None:
+        _check_tensor("slots", slots, torch.int64, (N,), dev)
+        a.pages, a.page_size = _check_cache(k_cache, v_cache, q.dtype, Hk, d, dev)
+        a.v_in = _rows("v", v, q.dtype, (N, Hk, d), dev)
+        a.slots, a.k_cache, a.v_cache = slots.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr()
+        if N == 0:
+            a.slots = None
+    elif k_cache is not None or v_cache is not None or v is not None:
+        raise ValueError("v, k_cache and v_cache need slots")
+    if q_out is None:
+        q_out = torch.empty((N, Hq, d), dtype=q.dtype, device=dev)
+    a.q_out = _rows("q_out", q_out, q.dtype, (N, Hq, d), dev)
+    if k_out is None and slots is None:
+        k_out = torch.empty((N, Hk, d), dtype=q.dtype, device=dev)
+    if k_out is not None:
+        a.k_out = _rows("k_out", k_out, q.dtype, (N, Hk, d), dev)
+    a.eps = float(eps)
+    with _on_device(dev):
+        a.stream = _stream(stream).value
+        check(lib().vda_qk_norm_rope(ctypes.byref(a)), "vda_qk_norm_rope")
+    return q_out, k_out
+
+
+def vda_qk_norm_rope_backward(dq_out, dk_out, q, k, q_weight=None, k_weight=None, positions=None, frequencies=None,
+                              axis=None, interleaved=False, eps=1e-6, dq=None, dk=None, workspace=None, stream=None):
+    """Gradient of `vda_qk_norm_rope`: from the gradients of its results
+    [N, heads, d] (strided, or broadcast with stride 0, as they come) and its
+    inputs, returns (dq, dk, dq_weight, dk_weight); the weight gradients are
+    float32 [d], sums in a fixed order (None for a weight that is None)."""
+    N, Hq, Hk, d, dt = _qk_shapes(q, k)
+    dev = q.device
+    a = VdaQkGradArgs()
+    a.dtype = dt
+    a.dq_out = _rows("dq_out", dq_out, q.dtype, (N, Hq, d), dev)
+    a.dk_out = _rows("dk_out", dk_out, q.dtype, (N, Hk, d), dev)
+    a.q_in = _rows("q", q, q.dtype, (N, Hq, d), dev)
+    a.k_in = _rows("k", k, q.dtype, (N, Hk, d), dev)
+    a.N, a.Hq, a.Hk, a.d = N, Hq, Hk, d
+    a.q_weight = _set_weight("q_weight", q_weight, d, dev)
+    a.k_weight = _set_weight("k_weight", k_weight, d, dev)
+    _set_rotation(a, N, positions, frequencies, axis, interleaved, dev)
+    if dq is None:
+        dq = torch.empty((N, Hq, d), dtype=q.dtype, device=dev)
+    if dk is None:
+        dk = torch.empty((N, Hk, d), dtype=q.dtype, device=dev)
+    a.dq_in = _rows("dq", dq, q.dtype, (N, Hq, d), dev)
+    a.dk_in = _rows("dk", dk, q.dtype, (N, Hk, d), dev)
+    L = lib()
+    dwq = torch.empty(d, dtype=torch.float32, device=dev) if q_weight is not None else None
+    dwk = torch.empty(d, dtype=torch.float32, device=dev) if k_weight is not None else None
+    a.dq_weight = dwq.data_ptr() if dwq is not None else None
+    a.dk_weight = dwk.data_ptr() if dwk is not None else None
+    if workspace is None and (dwq is not None or dwk is not None):
+        workspace = torch.empty(int(L.vda_qk_grad_workspace_bytes(d)), dtype=torch.uint8, device=dev)
+    a.eps = float(eps)
+    with _on_device(dev):
+        a.stream = _stream(stream).value
+        rc = L.vda_qk_norm_rope_backward(ctypes.byref(a), _ptr(workspace), 0 if workspace is None else workspace.numel())
+        check(rc, "vda_qk_norm_rope_backward")
+    return dq, dk, dwq, dwk
 
 
 def vda_text_state(k_text, v_text, beta_text, S_out=None, workspace=None, stream=None):

@@ -20,6 +20,7 @@
 #include "kernels_simt.cuh"
 #include "kernels_tc.cuh"
 #include "kernels_prep.cuh"
+#include "kernels_qk.cuh"
 
 namespace {
 
@@ -420,7 +421,134 @@ int launch_prep(const vda_prep_args& a, int nst) {
 }
 }  // namespace
 
+// ============================================================================
+// Softmax branch: argument checks shared by its entry points
+namespace {
+size_t elem_size(int dtype) { return dtype == VDA_BF16 ? 2 : 4; }
+
+// Rows that kernels read: aligned, strides >= 0 and multiples of 16 bytes
+// (a stride that nothing steps over is not looked at).
+bool rows_ok(const vda_rows& r, int64_t N, int64_t heads, size_t es) {
+  if (!r.data || !aligned16(r.data)) return false;
+  const int64_t m = (int64_t)(16 / es);
+  // the whole extent of an axis stays far inside 63 bits
+  const auto step_ok = [&](int64_t st, int64_t n) {
+    return n <= 1 || (st >= 0 && st % m == 0 && (double)st * (double)(n - 1) < 4.0e15);
+  };
+  return step_ok(r.token_stride, N) && step_ok(r.head_stride, heads);
+}
+
+// Rows that kernels write: moreover no two of them overlap, in either order
+// of the two axes.
+bool rows_out_ok(const vda_rows& r, int64_t N, int64_t heads, int64_t d, size_t es) {
+  if (!rows_ok(r, N, heads, es)) return false;
+  const auto nested = [&](int64_t s_in, int64_t n_in, int64_t s_out, int64_t n_out) {
+    const int64_t inner = n_in > 1 ? s_in : d;
+    if (inner < d) return false;
+    const int64_t extent = n_in > 1 ? s_in * (n_in - 1) + d : d;
+    return n_out <= 1 || s_out >= extent;
+  };
+  return nested(r.head_stride, heads, r.token_stride, N) || nested(r.token_stride, N, r.head_stride, heads);
+}
+
+int check_qk_sizes(int dtype, int N, int Hq, int Hk, int d, int axes, int rot, const int* positions,
+                   const double* frequencies, const int* axis) {
+  if (dtype != VDA_BF16 && dtype != VDA_F32) return VDA_ERR_INVALID_ARGUMENT;
+  if (N < 0 || Hq < 1 || Hk < 1 || d < 1 || rot < 0 || rot > d) return VDA_ERR_INVALID_ARGUMENT;
+  if (d != 16 && d != 32 && d != 64 && d != 128) return VDA_ERR_UNSUPPORTED;
+  if (rot % 16 != 0 || Hq > 65536 || Hk > 65536) return VDA_ERR_UNSUPPORTED;
+  if (rot > 0) {
+    if (axes < 1 || !frequencies || !axis || (N > 0 && !positions)) return VDA_ERR_INVALID_ARGUMENT;
+    if (reinterpret_cast<uintptr_t>(frequencies) % 8 || reinterpret_cast<uintptr_t>(axis) % 4 ||
+        reinterpret_cast<uintptr_t>(positions) % 4)
+      return VDA_ERR_INVALID_ARGUMENT;
+    if (axes > 8) return VDA_ERR_UNSUPPORTED;
+  }
+  return VDA_OK;
+}
+
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+template <typename T>
+int dispatch_qk_fwd(const vda_qk_args& a, float eps, int sms) {
+  switch (a.d) {
+    case 16: return vda::qk::launch_fwd<T, 16>(a, eps, sms);
+    case 32: return vda::qk::launch_fwd<T, 32>(a, eps, sms);
+    case 64: return vda::qk::launch_fwd<T, 64>(a, eps, sms);
+    default: return vda::qk::launch_fwd<T, 128>(a, eps, sms);
+  }
+}
+
+template <typename T>
+int dispatch_qk_bwd(const vda_qk_grad_args& a, float* part, float eps, int sms) {
+  switch (a.d) {
+    case 16: return vda::qk::launch_bwd<T, 16>(a, part, eps, sms);
+    case 32: return vda::qk::launch_bwd<T, 32>(a, part, eps, sms);
+    case 64: return vda::qk::launch_bwd<T, 64>(a, part, eps, sms);
+    default: return vda::qk::launch_bwd<T, 128>(a, part, eps, sms);
+  }
+}
+}  // namespace
+
 extern "C" {
+
+int vda_qk_norm_rope(const vda_qk_args* a) {
+  if (!a) return VDA_ERR_INVALID_ARGUMENT;
+  const int rc = check_qk_sizes(a->dtype, a->N, a->Hq, a->Hk, a->d, a->axes, a->rot, a->positions, a->frequencies,
+                                a->axis);
+  if (rc != VDA_OK) return rc;
+  if (!aligned4(a->q_weight) || !aligned4(a->k_weight)) return VDA_ERR_INVALID_ARGUMENT;
+  if (a->slots) {
+    if (!a->k_cache || !a->v_cache || !aligned16(a->k_cache) || !aligned16(a->v_cache) || a->pages < 1 ||
+        a->page_size < 1 || reinterpret_cast<uintptr_t>(a->slots) % 8)
+      return VDA_ERR_INVALID_ARGUMENT;
+    if ((double)a->pages * a->page_size * a->Hk * a->d > 4.0e15) return VDA_ERR_UNSUPPORTED;
+  }
+  if (a->N == 0) return VDA_OK;
+  const size_t es = elem_size(a->dtype);
+  if (!rows_ok(a->q_in, a->N, a->Hq, es) || !rows_ok(a->k_in, a->N, a->Hk, es) ||
+      !rows_out_ok(a->q_out, a->N, a->Hq, a->d, es))
+    return VDA_ERR_INVALID_ARGUMENT;
+  if ((!a->slots || a->k_out.data) && !rows_out_ok(a->k_out, a->N, a->Hk, a->d, es)) return VDA_ERR_INVALID_ARGUMENT;
+  if (a->slots && !rows_ok(a->v_in, a->N, a->Hk, es)) return VDA_ERR_INVALID_ARGUMENT;
+  const float eps = a->eps > 0.f ? a->eps : 1e-6f;
+  const int sms = vda::tc::num_sms();
+  return a->dtype == VDA_BF16 ? dispatch_qk_fwd<__nv_bfloat16>(*a, eps, sms) : dispatch_qk_fwd<float>(*a, eps, sms);
+}
+
+size_t vda_qk_grad_workspace_bytes(int d) {
+  if (d != 16 && d != 32 && d != 64 && d != 128) return 0;
+  return (size_t)vda::qk::kBwdMaxBlocks * 2 * d * sizeof(float);
+}
+
+int vda_qk_norm_rope_backward(const vda_qk_grad_args* a, void* workspace, size_t workspace_bytes) {
+  if (!a) return VDA_ERR_INVALID_ARGUMENT;
+  const int rc = check_qk_sizes(a->dtype, a->N, a->Hq, a->Hk, a->d, a->axes, a->rot, a->positions, a->frequencies,
+                                a->axis);
+  if (rc != VDA_OK) return rc;
+  if (!aligned4(a->q_weight) || !aligned4(a->k_weight) || !aligned4(a->dq_weight) || !aligned4(a->dk_weight))
+    return VDA_ERR_INVALID_ARGUMENT;
+  if (a->N == 0) {
+    cudaStream_t s = static_cast<cudaStream_t>(a->stream);
+    for (float* w : {a->dq_weight, a->dk_weight})
+      if (w && cudaMemsetAsync(w, 0, (size_t)a->d * sizeof(float), s) != cudaSuccess) return VDA_ERR_CUDA;
+    return VDA_OK;
+  }
+  const size_t es = elem_size(a->dtype);
+  if (!rows_ok(a->dq_out, a->N, a->Hq, es) || !rows_ok(a->dk_out, a->N, a->Hk, es) ||
+      !rows_ok(a->q_in, a->N, a->Hq, es) || !rows_ok(a->k_in, a->N, a->Hk, es) ||
+      !rows_out_ok(a->dq_in, a->N, a->Hq, a->d, es) || !rows_out_ok(a->dk_in, a->N, a->Hk, a->d, es))
+    return VDA_ERR_INVALID_ARGUMENT;
+  const bool sums = a->dq_weight || a->dk_weight;
+  if (sums && (!workspace || (reinterpret_cast<uintptr_t>(workspace) % kAlign) != 0 ||
+               workspace_bytes < vda_qk_grad_workspace_bytes(a->d)))
+    return VDA_ERR_WORKSPACE;
+  const float eps = a->eps > 0.f ? a->eps : 1e-6f;
+  const int sms = vda::tc::num_sms();
+  float* part = sums ? static_cast<float*>(workspace) : nullptr;
+  return a->dtype == VDA_BF16 ? dispatch_qk_bwd<__nv_bfloat16>(*a, part, eps, sms)
+                              : dispatch_qk_bwd<float>(*a, part, eps, sms);
+}
 
 int vda_prep(const vda_prep_args* a) {
   if (!a) return VDA_ERR_INVALID_ARGUMENT;

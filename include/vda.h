@@ -275,6 +275,94 @@ typedef struct vda_prep_args {
 
 VDA_API int vda_prep(const vda_prep_args* args);
 
+/* ---------------------------------------------------------------------------
+ * The Softmax branch of the hybrid block (Section 2.1 and the fused QK-norm +
+ * RoPE of Section 5): the norm and rotation of queries and keys, which may
+ * append K and V to a paged cache, and the attention that reads the cache.
+ *
+ * Rows of a tensor [N tokens, heads, d]: channel 0 of (token, head) lies at
+ * data + token * token_stride + head * head_stride (in elements, both >= 0),
+ * the d channels are contiguous.  data is 16-byte aligned and the strides are
+ * multiples of 16 bytes, so slices of a joint [q | k | v] projection and
+ * head-major tensors are taken as they are.  Inputs may have stride 0
+ * (broadcast); rows of outputs must not overlap, neither one another nor an
+ * input. */
+typedef struct vda_rows {
+  void* data;
+  int64_t token_stride;
+  int64_t head_stride;
+} vda_rows;
+
+/* For every token and head, with x its d channels and w the tensor's weight:
+ *   x^ = x / sqrt(mean(x^2) + eps),  z = w x^,  y = R z
+ * R turns pair p of the first rot channels by position[axis[p]] * frequencies[p]:
+ *   (y_i, y_j) = (z_i cos - z_j sin, z_j cos + z_i sin),
+ *   (i, j) = (p, p + rot / 2), or (2 p, 2 p + 1) when interleaved.
+ * Sums and angles are held in 32 bits or more; the phase of an integer
+ * position is exact to position * 2^-55 turns.  y is rounded once.
+ * With slots set, k's y and v (unchanged) also go to place slots[token] =
+ * page * page_size + offset of the paged cache [pages, Hk, page_size, d]; a
+ * token whose slot lies outside [0, pages * page_size) is not stored (give -1
+ * for padding), and two tokens must not share a slot.
+ * Supported: d in {16, 32, 64, 128}, rot a multiple of 16 in [0, d], axes in
+ * 1..8.  N = 0 is a valid empty call.  Returns vda_status. */
+typedef struct vda_qk_args {
+  int dtype;                  /* vda_dtype of q, k, v and the cache */
+  vda_rows q_in;              /* [N, Hq, d] */
+  vda_rows k_in;              /* [N, Hk, d] */
+  vda_rows v_in;              /* [N, Hk, d], read only when slots is set */
+  vda_rows q_out;             /* [N, Hq, d] */
+  vda_rows k_out;             /* [N, Hk, d]; data may be NULL when slots is set */
+  const float* q_weight;      /* [d] or NULL: ones */
+  const float* k_weight;      /* [d] or NULL: ones */
+  const int* positions;       /* [N, axes]; NULL when rot = 0 */
+  const double* frequencies;  /* [rot / 2] radians per position; NULL when rot = 0 */
+  const int* axis;            /* [rot / 2] axis of each pair (outside [0, axes): not turned); NULL when rot = 0 */
+  const int64_t* slots;       /* [N] or NULL: no cache */
+  void* k_cache;              /* [pages, Hk, page_size, d] */
+  void* v_cache;              /* [pages, Hk, page_size, d] */
+  int N, Hq, Hk, d;
+  int axes, rot, interleaved;
+  int pages, page_size;       /* >= 1 when slots is set */
+  float eps;                  /* <= 0 selects 1e-6 */
+  void* stream;               /* cudaStream_t */
+} vda_qk_args;
+
+VDA_API int vda_qk_norm_rope(const vda_qk_args* args);
+
+/* Gradient of vda_qk_norm_rope: from the gradients of q_out and k_out and the
+ * forward's inputs, the gradients of q_in and k_in and of the weights,
+ *   g = R^T dy,  dw = sum over tokens and heads of g x^,
+ *   dx = (g w - x^ mean(g w x^)) / sqrt(mean(x^2) + eps).
+ * The norm is computed again from q_in and k_in.  The weight gradients are
+ * float32 sums in a fixed order: the same inputs give the same bits.
+ * Workspace: vda_qk_grad_workspace_bytes(d), device, 256-byte aligned; it may
+ * be NULL when both weight gradients are.  N = 0 sets the weight gradients to
+ * zero. */
+typedef struct vda_qk_grad_args {
+  int dtype;
+  vda_rows dq_out;            /* [N, Hq, d] gradient of q_out */
+  vda_rows dk_out;            /* [N, Hk, d] gradient of k_out */
+  vda_rows q_in;              /* [N, Hq, d] */
+  vda_rows k_in;              /* [N, Hk, d] */
+  vda_rows dq_in;             /* [N, Hq, d] result */
+  vda_rows dk_in;             /* [N, Hk, d] result */
+  const float* q_weight;
+  const float* k_weight;
+  float* dq_weight;           /* [d] result, or NULL */
+  float* dk_weight;           /* [d] result, or NULL */
+  const int* positions;
+  const double* frequencies;
+  const int* axis;
+  int N, Hq, Hk, d;
+  int axes, rot, interleaved;
+  float eps;
+  void* stream;
+} vda_qk_grad_args;
+
+VDA_API size_t vda_qk_grad_workspace_bytes(int d);
+VDA_API int vda_qk_norm_rope_backward(const vda_qk_grad_args* args, void* workspace, size_t workspace_bytes);
+
 /* Human-readable name of a vda_status value. */
 VDA_API const char* vda_status_string(int status);
 
