@@ -96,6 +96,22 @@ class VdaQkGradArgs(ctypes.Structure):
     ]
 
 
+class VdaAttnArgs(ctypes.Structure):
+    """Mirror of `vda_attn_args` in include/vda.h."""
+    _fields_ = [
+        ("dtype", c_int),
+        ("q", VdaRows), ("k_cache", c_void_p), ("v_cache", c_void_p),
+        ("block_table", c_void_p), ("kv_len", c_void_p), ("q_start", c_void_p),
+        ("out", VdaRows), ("lse", c_void_p),
+        ("table_stride", c_int64),
+        ("N", c_int), ("B", c_int), ("Hq", c_int), ("Hk", c_int), ("d", c_int),
+        ("pages", c_int), ("page_size", c_int), ("max_pages", c_int),
+        ("block", c_int), ("window_blocks", c_int), ("anchors", c_int),
+        ("scale", c_float),
+        ("stream", c_void_p),
+    ]
+
+
 _SIGNATURES = {
     "vda_forward": (c_int, [c_void_p] * 8 + [c_int] * 8 + [c_void_p, c_void_p]),
     "vda_forward_f32": (c_int, [c_void_p] * 8 + [c_int] * 8 + [c_void_p, c_void_p]),
@@ -116,6 +132,8 @@ _SIGNATURES = {
     "vda_qk_norm_rope": (c_int, [ctypes.POINTER(VdaQkArgs)]),
     "vda_qk_grad_workspace_bytes": (c_size_t, [c_int]),
     "vda_qk_norm_rope_backward": (c_int, [ctypes.POINTER(VdaQkGradArgs), c_void_p, c_size_t]),
+    "vda_paged_attention_workspace_bytes": (c_size_t, [c_int] * 7),
+    "vda_paged_attention": (c_int, [ctypes.POINTER(VdaAttnArgs), c_void_p, c_size_t]),
     "vda_selftest_wait_timeout": (c_int, [c_int, c_void_p]),
 }
 

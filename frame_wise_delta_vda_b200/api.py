@@ -12,7 +12,7 @@ import ctypes
 
 import torch
 
-from ._lib import (VDA_BF16, VDA_F32, VDA_SCAN_AUTO, VDA_SCAN_CHUNKS, VDA_SCAN_FRAMES, VdaArgs,  # noqa: F401
+from ._lib import (VDA_BF16, VDA_F32, VDA_SCAN_AUTO, VDA_SCAN_CHUNKS, VDA_SCAN_FRAMES, VdaArgs, VdaAttnArgs,  # noqa: F401
                    VdaError, VdaPrepArgs, VdaQkArgs, VdaQkGradArgs, VdaRows, check, lib)
 
 _SCAN_FORMS = {"auto": VDA_SCAN_AUTO, "frames": VDA_SCAN_FRAMES, "chunks": VDA_SCAN_CHUNKS}
@@ -342,6 +342,73 @@ def vda_qk_norm_rope_backward(dq_out, dk_out, q, k, q_weight=None, k_weight=None
         rc = L.vda_qk_norm_rope_backward(ctypes.byref(a), _ptr(workspace), 0 if workspace is None else workspace.numel())
         check(rc, "vda_qk_norm_rope_backward")
     return dq, dk, dwq, dwk
+
+
+def vda_paged_attention_workspace_bytes(N, B, Hq, Hk, d, page_size, dtype=torch.bfloat16):
+    return int(lib().vda_paged_attention_workspace_bytes(_DTYPES[dtype], N, B, Hq, Hk, d, page_size))
+
+
+def vda_paged_attention(q, k_cache, v_cache, block_table, kv_len, q_start, block=1, window_blocks=-1, anchors=0,
+                        scale=None, out=None, lse=None, return_lse=False, workspace=None, stream=None):
+    """Attention of the new tokens q [N, Hq, d] of B sequences over the paged
+    cache k_cache, v_cache [pages, Hk, page_size, d], which holds their keys
+    already (see include/vda.h).  block_table [B, max_pages], kv_len [B] and
+    q_start [B + 1] are int32 on the device; sequence b's new tokens are rows
+    q_start[b] .. q_start[b + 1] and its last positions.  `block` 1 is causal
+    by token, n >= 2 by blocks of n tokens, 0 sees every key; `window_blocks`
+    blocks before a token's own are seen (-1: all) besides the first `anchors`
+    keys.  Returns out [N, Hq, d], or (out, lse [N, Hq] float32) with
+    return_lse.  Calls that may overlap need workspaces of their own (the
+    default is a new one)."""
+    if q.dim() != 3:
+        raise ValueError("q must be [N, Hq, d]")
+    N, Hq, d = q.shape
+    dt = _DTYPES.get(q.dtype)
+    if dt is None:
+        raise ValueError(f"unsupported dtype {q.dtype} (bf16 or float32)")
+    dev = q.device
+    if k_cache is None or k_cache.dim() != 4:
+        raise ValueError("k_cache and v_cache must be [pages, Hk, page_size, d]")
+    Hk = k_cache.shape[1]
+    pages, page = _check_cache(k_cache, v_cache, q.dtype, Hk, d, dev)
+    if block_table is None or block_table.dim() != 2:
+        raise ValueError("block_table must be [B, max_pages]")
+    B, max_pages = block_table.shape
+    if not block_table.is_cuda or block_table.device != dev or block_table.dtype != torch.int32:
+        raise ValueError(f"block_table must be int32 on {dev}")
+    if max_pages > 1 and block_table.stride(1) != 1:
+        raise ValueError("block_table must have contiguous rows")
+    _check_tensor("kv_len", kv_len, torch.int32, (B,), dev)
+    _check_tensor("q_start", q_start, torch.int32, (B + 1,), dev)
+    a = VdaAttnArgs()
+    a.dtype = dt
+    a.q = _rows("q", q, q.dtype, (N, Hq, d), dev)
+    if out is None:
+        out = torch.empty((N, Hq, d), dtype=q.dtype, device=dev)
+    a.out = _rows("out", out, q.dtype, (N, Hq, d), dev)
+    if lse is None and return_lse:
+        lse = torch.empty((N, Hq), dtype=torch.float32, device=dev)
+    if lse is not None:
+        _check_tensor("lse", lse, torch.float32, (N, Hq), dev)
+        a.lse = lse.data_ptr()
+    a.k_cache, a.v_cache = k_cache.data_ptr(), v_cache.data_ptr()
+    a.block_table, a.kv_len, a.q_start = block_table.data_ptr(), kv_len.data_ptr(), q_start.data_ptr()
+    a.table_stride = block_table.stride(0)
+    a.N, a.B, a.Hq, a.Hk, a.d = N, B, Hq, Hk, d
+    a.pages, a.page_size, a.max_pages = pages, page, max_pages
+    a.block, a.window_blocks, a.anchors = int(block), int(window_blocks), int(anchors)
+    if scale is not None:
+        a.scale = float(scale)
+        if not a.scale > 0.0:
+            raise ValueError(f"scale must be positive, got {scale}")
+    L = lib()
+    with _on_device(dev):
+        if workspace is None:
+            n = int(L.vda_paged_attention_workspace_bytes(dt, N, B, Hq, Hk, d, page))
+            workspace = torch.empty(n, dtype=torch.uint8, device=dev)
+        a.stream = _stream(stream).value
+        check(L.vda_paged_attention(ctypes.byref(a), _ptr(workspace), workspace.numel()), "vda_paged_attention")
+    return (out, lse) if return_lse else out
 
 
 def vda_text_state(k_text, v_text, beta_text, S_out=None, workspace=None, stream=None):

@@ -10,6 +10,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <cmath>
 #include <cstdio>
 #include <cstring>
 #include <mutex>
@@ -21,6 +22,7 @@
 #include "kernels_tc.cuh"
 #include "kernels_prep.cuh"
 #include "kernels_qk.cuh"
+#include "kernels_attn_tc.cuh"
 
 namespace {
 
@@ -488,9 +490,67 @@ int dispatch_qk_bwd(const vda_qk_grad_args& a, float* part, float eps, int sms) 
     default: return vda::qk::launch_bwd<T, 128>(a, part, eps, sms);
   }
 }
+
+int check_attn_sizes(int dtype, int N, int B, int Hq, int Hk, int d, int page) {
+  if (dtype != VDA_BF16 && dtype != VDA_F32) return VDA_ERR_INVALID_ARGUMENT;
+  if (N < 0 || B < 1 || Hq < 1 || Hk < 1 || d < 1 || page < 1 || Hq % Hk != 0) return VDA_ERR_INVALID_ARGUMENT;
+  if (d != 16 && d != 32 && d != 64 && d != 128) return VDA_ERR_UNSUPPORTED;
+  const int G = Hq / Hk;
+  if (!vda::attn::tc_supported(dtype, d, G, page) && G > 64) return VDA_ERR_UNSUPPORTED;
+  if ((double)N * Hq > 2.0e9 || Hq > 65536) return VDA_ERR_UNSUPPORTED;
+  return VDA_OK;
+}
+
+template <typename T>
+int dispatch_attn_simt(const vda_attn_args& a, const vda::attn::AttnPlan& p, char* ws, float c2) {
+  switch (a.d) {
+    case 16: return vda::attn::launch_attn_simt<T, 16>(a, p, ws, c2);
+    case 32: return vda::attn::launch_attn_simt<T, 32>(a, p, ws, c2);
+    case 64: return vda::attn::launch_attn_simt<T, 64>(a, p, ws, c2);
+    default: return vda::attn::launch_attn_simt<T, 128>(a, p, ws, c2);
+  }
+}
 }  // namespace
 
 extern "C" {
+
+size_t vda_paged_attention_workspace_bytes(int dtype, int N, int B, int Hq, int Hk, int d, int page_size) {
+  if (check_attn_sizes(dtype, N, B, Hq, Hk, d, page_size) != VDA_OK) return 0;
+  return vda::attn::make_attn_plan(dtype, Hq, Hk, d, page_size, N, B, vda::tc::num_sms()).total;
+}
+
+int vda_paged_attention(const vda_attn_args* a, void* workspace, size_t workspace_bytes) {
+  if (!a) return VDA_ERR_INVALID_ARGUMENT;
+  const int rc = check_attn_sizes(a->dtype, a->N, a->B, a->Hq, a->Hk, a->d, a->page_size);
+  if (rc != VDA_OK) return rc;
+  if (a->pages < 1 || a->max_pages < 1 || a->table_stride < 0 || a->block < 0 || a->anchors < 0 ||
+      !(a->scale >= 0.f && a->scale < 1e30f))
+    return VDA_ERR_INVALID_ARGUMENT;
+  if (a->block > (1 << 30) || a->anchors > (1 << 30) || (double)a->pages * a->Hk > 2147483647.0 ||
+      (double)a->pages * a->Hk * a->page_size * a->d > 4.0e15)
+    return VDA_ERR_UNSUPPORTED;
+  if (!a->k_cache || !a->v_cache || !aligned16(a->k_cache) || !aligned16(a->v_cache)) return VDA_ERR_INVALID_ARGUMENT;
+  if (!a->block_table || !a->kv_len || !a->q_start || !aligned4(a->block_table) || !aligned4(a->kv_len) ||
+      !aligned4(a->q_start) || !aligned4(a->lse))
+    return VDA_ERR_INVALID_ARGUMENT;
+  if (a->N == 0) return VDA_OK;
+  const size_t es = elem_size(a->dtype);
+  if (!rows_ok(a->q, a->N, a->Hq, es) || !rows_out_ok(a->out, a->N, a->Hq, a->d, es)) return VDA_ERR_INVALID_ARGUMENT;
+  const vda::attn::AttnPlan p =
+      vda::attn::make_attn_plan(a->dtype, a->Hq, a->Hk, a->d, a->page_size, a->N, a->B, vda::tc::num_sms());
+  // the tensor map of q steps over at least 16 and less than 2^40 bytes
+  if (p.tc && ((a->N > 1 && (a->q.token_stride < 8 || a->q.token_stride >= (1LL << 39))) ||
+               (a->Hq > 1 && (a->q.head_stride < 8 || a->q.head_stride >= (1LL << 39)))))
+    return VDA_ERR_UNSUPPORTED;
+  if (!workspace || (reinterpret_cast<uintptr_t>(workspace) % kAlign) != 0 || workspace_bytes < p.total)
+    return VDA_ERR_WORKSPACE;
+  char* ws = static_cast<char*>(workspace);
+  // exponents in base 2
+  const float scale = a->scale > 0.f ? a->scale : 1.f / sqrtf((float)a->d);
+  const float c2 = scale * vda::attn::kLog2e;
+  if (p.tc) return a->d == 128 ? vda::attn::launch_attn_tc<128>(*a, p, ws, c2) : vda::attn::launch_attn_tc<64>(*a, p, ws, c2);
+  return a->dtype == VDA_BF16 ? dispatch_attn_simt<__nv_bfloat16>(*a, p, ws, c2) : dispatch_attn_simt<float>(*a, p, ws, c2);
+}
 
 int vda_qk_norm_rope(const vda_qk_args* a) {
   if (!a) return VDA_ERR_INVALID_ARGUMENT;

@@ -363,6 +363,58 @@ typedef struct vda_qk_grad_args {
 VDA_API size_t vda_qk_grad_workspace_bytes(int d);
 VDA_API int vda_qk_norm_rope_backward(const vda_qk_grad_args* args, void* workspace, size_t workspace_bytes);
 
+/* Attention of new tokens over a paged cache that already holds their keys
+ * and values (vda_qk_norm_rope with slots puts them there).  The n = q_start[b +
+ * 1] - q_start[b] new tokens of sequence b are its last n positions: token i
+ * stands at position p = kv_len[b] - n + i.  Key j of sequence b lies in page
+ * block_table[b][j / page_size] at offset j % page_size.
+ *   o = sum_j softmax_j(scale q k_j) v_j,  lse = log sum_j exp(scale q k_j)
+ * over the keys j < kv_len[b] that the token sees:
+ *   block = 0:  all of them;
+ *   block >= 1: positions fall into blocks floor((p - anchors) / block); the
+ *               token sees its own block whole (block = 1: causal by token,
+ *               block = tokens of a chunk: causal by chunk), the window_blocks
+ *               blocks before it (< 0: every block before it) and the first
+ *               `anchors` keys.
+ * A token that sees nothing (p < 0, or no key) gets o = 0 and lse = -inf.  A
+ * key whose page id lies outside [0, pages) is not seen, whatever mask holds
+ * (an evicted page).  What lies in the cache at places that no new token of
+ * the sequence sees does not matter, NaN included; a value that is not finite
+ * at a key which one token sees can reach the other tokens of the sequence.
+ * Query heads h with h / (Hq / Hk) equal share a KV head.  Tokens before
+ * q_start[0] and from q_start[B] on are left as they were.
+ * q, out, lse: rows as described above; lse [N, Hq] float32 contiguous or NULL.
+ * S, the softmax's maximum and sum and the output sums are float32; on the
+ * tensor cores (bf16, d = 64 or 128, page_size a power of two from 8 to 128 or a
+ * multiple of 128) the weights are rounded to bf16 before their product with
+ * V, their sum is not.  Other types and sizes run on a SIMT kernel in float32.
+ * Supported: d in {16, 32, 64, 128}; Hq / Hk up to 128 on the tensor cores,
+ * 64 elsewhere; pages * Hk < 2^31.  The lengths and the table are read on the
+ * device: a captured call follows them.  N = 0 is a valid empty call.
+ * Workspace: vda_paged_attention_workspace_bytes(), device, 256-byte aligned;
+ * calls that may overlap need one each.  Returns vda_status. */
+typedef struct vda_attn_args {
+  int dtype;                  /* vda_dtype of q, the cache and out */
+  vda_rows q;                 /* [N, Hq, d] */
+  const void* k_cache;        /* [pages, Hk, page_size, d] */
+  const void* v_cache;        /* [pages, Hk, page_size, d] */
+  const int* block_table;     /* [B, max_pages], rows table_stride apart */
+  const int* kv_len;          /* [B] keys of each sequence, the new tokens' among them */
+  const int* q_start;         /* [B + 1] first new token of each sequence, ascending */
+  vda_rows out;               /* [N, Hq, d] */
+  float* lse;                 /* [N, Hq] or NULL */
+  int64_t table_stride;
+  int N, B, Hq, Hk, d;
+  int pages, page_size, max_pages;
+  int block, window_blocks, anchors;
+  float scale;                /* > 0; 0 selects 1 / sqrt(d) */
+  void* stream;               /* cudaStream_t */
+} vda_attn_args;
+
+/* 0 when the sizes are invalid or unsupported. */
+VDA_API size_t vda_paged_attention_workspace_bytes(int dtype, int N, int B, int Hq, int Hk, int d, int page_size);
+VDA_API int vda_paged_attention(const vda_attn_args* args, void* workspace, size_t workspace_bytes);
+
 /* Human-readable name of a vda_status value. */
 VDA_API const char* vda_status_string(int status);
 

@@ -7,7 +7,7 @@ import re
 import pytest
 
 from frame_wise_delta_vda_b200 import _lib
-from frame_wise_delta_vda_b200._lib import VdaQkArgs, VdaQkGradArgs, VdaRows
+from frame_wise_delta_vda_b200._lib import VdaAttnArgs, VdaQkArgs, VdaQkGradArgs, VdaRows
 
 P = 1 << 20   # an aligned address that nothing reads
 
@@ -28,7 +28,7 @@ def header_fields(struct):
 
 
 @pytest.mark.parametrize("struct,mirror", [("vda_rows", VdaRows), ("vda_qk_args", VdaQkArgs),
-                                           ("vda_qk_grad_args", VdaQkGradArgs)])
+                                           ("vda_qk_grad_args", VdaQkGradArgs), ("vda_attn_args", VdaAttnArgs)])
 def test_argument_structs_mirror_the_header(struct, mirror):
     assert header_fields(struct) == [f[0] for f in mirror._fields_]
 
@@ -112,3 +112,50 @@ def test_qk_backward_workspace(L):
     for ws, size in ((None, n), (P, n - 1), (P + 128, n)):
         assert L.vda_qk_norm_rope_backward(ctypes.byref(grad_args()), ws, size) == WORKSPACE
     assert L.vda_qk_norm_rope_backward(None, P, n) == INVALID
+
+
+def attn_args(**over):
+    a = VdaAttnArgs()
+    a.dtype, a.N, a.B, a.Hq, a.Hk, a.d = 0, 10, 2, 4, 2, 64
+    a.q, a.out = rows(4, 64), rows(4, 64)
+    a.k_cache = a.v_cache = a.block_table = a.kv_len = a.q_start = a.lse = P
+    a.table_stride, a.pages, a.page_size, a.max_pages = 5, 9, 16, 5
+    a.block, a.window_blocks = 1, -1
+    for k, v in over.items():
+        setattr(a, k, v)
+    return a
+
+
+@pytest.mark.parametrize("over,status", [
+    (dict(dtype=2), INVALID), (dict(N=-1), INVALID), (dict(B=0), INVALID), (dict(Hq=0), INVALID), (dict(Hk=0), INVALID),
+    (dict(Hq=3), INVALID), (dict(d=0), INVALID), (dict(d=96), UNSUPPORTED), (dict(pages=0), INVALID),
+    (dict(page_size=0), INVALID), (dict(max_pages=0), INVALID), (dict(table_stride=-1), INVALID),
+    (dict(block=-1), INVALID), (dict(anchors=-1), INVALID), (dict(block=(1 << 30) + 1), UNSUPPORTED),
+    (dict(anchors=(1 << 30) + 1), UNSUPPORTED), (dict(pages=1 << 30), UNSUPPORTED),
+    (dict(scale=-1.0), INVALID), (dict(scale=float("nan")), INVALID), (dict(scale=float("inf")), INVALID),
+    (dict(k_cache=None), INVALID), (dict(v_cache=P + 8), INVALID), (dict(block_table=None), INVALID),
+    (dict(kv_len=P + 2), INVALID), (dict(q_start=None), INVALID), (dict(lse=P + 1), INVALID),
+    (dict(q=rows(4, 64, data=0)), INVALID), (dict(q=VdaRows(P, 260, 64)), INVALID),
+    (dict(q=VdaRows(P, 0, 64)), UNSUPPORTED), (dict(q=VdaRows(P, 256, 0)), UNSUPPORTED),
+    (dict(q=VdaRows(P, 1 << 40, 64)), UNSUPPORTED),
+    (dict(out=VdaRows(P, 256, 0)), INVALID), (dict(out=VdaRows(P, 192, 64)), INVALID),
+    (dict(Hq=129, Hk=1), UNSUPPORTED), (dict(Hq=65, Hk=1, dtype=1), UNSUPPORTED),
+    (dict(Hq=65, Hk=1, page_size=17), UNSUPPORTED), (dict(N=1 << 30), UNSUPPORTED),
+])
+def test_paged_attention_refuses(L, over, status):
+    n = 1 << 40
+    assert L.vda_paged_attention(ctypes.byref(attn_args(**over)), P, n) == status
+
+
+def test_paged_attention_workspace(L):
+    assert L.vda_paged_attention_workspace_bytes(0, 10, 2, 4, 2, 96, 16) == 0
+    assert L.vda_paged_attention_workspace_bytes(0, 10, 2, 5, 2, 64, 16) == 0
+    for dtype, page in ((0, 16), (0, 17), (1, 16)):
+        n = L.vda_paged_attention_workspace_bytes(dtype, 10, 2, 4, 2, 64, page)
+        assert n > 0
+        for ws, size in ((None, n), (P, n - 1), (P + 128, n)):
+            a = attn_args(dtype=dtype, page_size=page)
+            assert L.vda_paged_attention(ctypes.byref(a), ws, size) == WORKSPACE
+    assert L.vda_paged_attention(None, P, 1) == INVALID
+    z = VdaRows()
+    assert L.vda_paged_attention(ctypes.byref(attn_args(N=0, q=z, out=z)), None, 0) == 0
