@@ -9,6 +9,7 @@ from __future__ import annotations
 import ctypes
 import os
 import re
+import struct
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libvda.so")
@@ -112,6 +113,24 @@ class VdaAttnArgs(ctypes.Structure):
     ]
 
 
+def packer(mirror):
+    """`struct.Struct` that packs the fields of a mirror (nested rows in
+    place, NULL as 0) into the bytes of the C struct: one call, where setting
+    thirty fields of the mirror one by one takes longer than the kernel."""
+    codes = {c_int: "i", c_float: "f", c_void_p: "P", c_int64: "q"}
+
+    def fmt(m):
+        return "".join(fmt(t) if issubclass(t, ctypes.Structure) else codes[t] for _, t in m._fields_)
+
+    s = struct.Struct("@" + fmt(mirror) + "0P")   # native alignment, the end padded to a pointer's
+    if s.size != ctypes.sizeof(mirror):
+        raise RuntimeError(f"{mirror.__name__}: packed size {s.size} is not {ctypes.sizeof(mirror)}")
+    return s.pack
+
+
+pack_qk, pack_qk_grad, pack_attn = packer(VdaQkArgs), packer(VdaQkGradArgs), packer(VdaAttnArgs)
+
+# The entry points of the Softmax branch take the argument block as packed bytes.
 _SIGNATURES = {
     "vda_forward": (c_int, [c_void_p] * 8 + [c_int] * 8 + [c_void_p, c_void_p]),
     "vda_forward_f32": (c_int, [c_void_p] * 8 + [c_int] * 8 + [c_void_p, c_void_p]),
@@ -129,11 +148,11 @@ _SIGNATURES = {
     "vda_launches_per_forward": (c_int, [c_int] * 8),
     "vda_status_string": (ctypes.c_char_p, [c_int]),
     "vda_prep": (c_int, [ctypes.POINTER(VdaPrepArgs)]),
-    "vda_qk_norm_rope": (c_int, [ctypes.POINTER(VdaQkArgs)]),
+    "vda_qk_norm_rope": (c_int, [c_void_p]),
     "vda_qk_grad_workspace_bytes": (c_size_t, [c_int]),
-    "vda_qk_norm_rope_backward": (c_int, [ctypes.POINTER(VdaQkGradArgs), c_void_p, c_size_t]),
+    "vda_qk_norm_rope_backward": (c_int, [c_void_p, c_void_p, c_size_t]),
     "vda_paged_attention_workspace_bytes": (c_size_t, [c_int] * 7),
-    "vda_paged_attention": (c_int, [ctypes.POINTER(VdaAttnArgs), c_void_p, c_size_t]),
+    "vda_paged_attention": (c_int, [c_void_p, c_void_p, c_size_t]),
     "vda_selftest_wait_timeout": (c_int, [c_int, c_void_p]),
 }
 

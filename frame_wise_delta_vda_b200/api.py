@@ -7,13 +7,13 @@ CUDA kernels; there is no PyTorch or CPU implementation here.
 
 from __future__ import annotations
 
-import contextlib
 import ctypes
+import struct
 
 import torch
 
-from ._lib import (VDA_BF16, VDA_F32, VDA_SCAN_AUTO, VDA_SCAN_CHUNKS, VDA_SCAN_FRAMES, VdaArgs, VdaAttnArgs,  # noqa: F401
-                   VdaError, VdaPrepArgs, VdaQkArgs, VdaQkGradArgs, VdaRows, check, lib)
+from ._lib import (VDA_BF16, VDA_F32, VDA_SCAN_AUTO, VDA_SCAN_CHUNKS, VDA_SCAN_FRAMES, VdaArgs,  # noqa: F401
+                   VdaError, VdaPrepArgs, check, lib, pack_attn, pack_qk, pack_qk_grad)
 
 _SCAN_FORMS = {"auto": VDA_SCAN_AUTO, "frames": VDA_SCAN_FRAMES, "chunks": VDA_SCAN_CHUNKS}
 
@@ -173,30 +173,55 @@ def vda_prep(q_in, k_in, v_in, wk_s, wk_t, wv_s, wv_t, Hl, Wl, q_out=None, k_out
 
 
 # ---------------------------------------------------------------------------
-# Softmax branch: norm and rotation of queries and keys, paged cache, attention
-def _on_device(device):
-    """The device the library launches on, which is the current one."""
-    if device.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
-    return torch.cuda.device(device)
+# Softmax branch: norm and rotation of queries and keys, paged cache, attention.
+#
+# A serving step makes these calls once a layer on a handful of tokens, where
+# the kernel takes a few microseconds: a tensor that is as it should be is
+# looked at once, and only one that is not goes through the checks that say why.
+def _call(index, fn, *args):
+    """fn(*args) with device `index` current, as the library launches there."""
+    if torch._C._cuda_getDevice() == index:
+        return fn(*args)
+    with torch.cuda.device(index):
+        return fn(*args)
 
 
-def _rows(name, t, dtype, shape, device):
-    """[N, heads, d] with contiguous channels, any token and head strides."""
+def _raw_stream(index, stream):
+    return torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+
+
+def _pack(pack, *fields):
+    try:
+        return pack(*fields)
+    except struct.error as e:   # a size that its C type does not hold
+        raise ValueError(f"argument out of range: {e}") from None
+
+
+def _at(name, t, dtype, shape, index):
+    """Address of a contiguous tensor on device `index`."""
+    if t is not None and t.dtype is dtype and t.get_device() == index and t.shape == shape and t.is_contiguous():
+        return t.data_ptr()
+    _check_tensor(name, t, dtype, shape, torch.device("cuda", index))
+    return t.data_ptr()
+
+
+def _rows(name, t, dtype, shape, index):
+    """(address, token stride, head stride) of [N, heads, d] with contiguous
+    channels and any token and head strides."""
+    if t is not None and t.dtype is dtype and t.get_device() == index and t.shape == shape:
+        st = t.stride()
+        if st[2] == 1:
+            return t.data_ptr(), st[0], st[1]
+        raise ValueError(f"{name} must have contiguous channels")
     if t is None:
         raise ValueError(f"{name} is required")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
     if t.dtype != dtype:
         raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
-    st = t.stride()
-    if st[2] != 1:
-        raise ValueError(f"{name} must have contiguous channels")
-    return VdaRows(t.data_ptr(), st[0], st[1])
+    raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
 
 
 def rope_frequencies(rot, theta=10000.0, sections=None, device="cuda"):
@@ -215,50 +240,43 @@ def rope_frequencies(rot, theta=10000.0, sections=None, device="cuda"):
             torch.tensor(axis, dtype=torch.int32, device=device))
 
 
-def _set_rotation(a, N, positions, frequencies, axis, interleaved, dev):
+def _rotation(N, positions, frequencies, axis, index):
+    """(positions, frequencies, axis, axes, rot) of the argument block."""
     if frequencies is None:
         if positions is not None or axis is not None:
             raise ValueError("positions and axis need frequencies")
-        return
-    rot = 2 * frequencies.numel()
-    _check_tensor("frequencies", frequencies, torch.float64, (rot // 2,), dev)
-    if axis is not None:
-        _check_tensor("axis", axis, torch.int32, (rot // 2,), dev)
+        return 0, 0, 0, 0, 0
+    half = frequencies.numel()
     if positions is None or positions.dim() != 2:
         raise ValueError("positions must be [N, axes]")
-    _check_tensor("positions", positions, torch.int32, (N, positions.shape[1]), dev)
-    if axis is None:
-        raise ValueError("axis is required with frequencies")
-    a.axes, a.rot, a.interleaved = positions.shape[1], rot, int(bool(interleaved))
-    if rot:
-        a.positions, a.frequencies, a.axis = positions.data_ptr(), frequencies.data_ptr(), axis.data_ptr()
+    axes = positions.shape[1]
+    return (_at("positions", positions, torch.int32, (N, axes), index),
+            _at("frequencies", frequencies, torch.float64, (half,), index),
+            _at("axis", axis, torch.int32, (half,), index), axes, 2 * half)
 
 
-def _set_weight(name, w, d, dev):
-    if w is None:
-        return None
-    _check_tensor(name, w, torch.float32, (d,), dev)
-    return w.data_ptr()
+def _weight(name, w, d, index):
+    return 0 if w is None else _at(name, w, torch.float32, (d,), index)
 
 
 def _qk_shapes(q, k):
     if q.dim() != 3 or k.dim() != 3:
         raise ValueError("q and k must be [N, heads, d]")
-    N, Hq, d = q.shape
+    if not q.is_cuda:
+        raise ValueError("q must be a CUDA tensor")
     dt = _DTYPES.get(q.dtype)
     if dt is None:
         raise ValueError(f"unsupported dtype {q.dtype} (bf16 or float32)")
+    N, Hq, d = q.shape
     return N, Hq, k.shape[1], d, dt
 
 
-def _check_cache(k_cache, v_cache, dtype, Hk, d, dev):
-    """[pages, Hk, page_size, d], contiguous: (pages, page_size)."""
+def _cache(k_cache, v_cache, dtype, Hk, d, index):
+    """(k_cache, v_cache, pages, page_size) of [pages, Hk, page_size, d], contiguous."""
     if k_cache is None or v_cache is None or k_cache.dim() != 4:
         raise ValueError("k_cache and v_cache must be [pages, Hk, page_size, d]")
-    pages, _, page, _ = k_cache.shape
-    _check_tensor("k_cache", k_cache, dtype, (pages, Hk, page, d), dev)
-    _check_tensor("v_cache", v_cache, dtype, (pages, Hk, page, d), dev)
-    return pages, page
+    shape = (k_cache.shape[0], Hk, k_cache.shape[2], d)
+    return (_at("k_cache", k_cache, dtype, shape, index), _at("v_cache", v_cache, dtype, shape, index), shape[0], shape[2])
 
 
 def vda_qk_norm_rope(q, k, q_weight=None, k_weight=None, positions=None, frequencies=None, axis=None,
@@ -273,35 +291,28 @@ def vda_qk_norm_rope(q, k, q_weight=None, k_weight=None, positions=None, frequen
     * page_size + offset; -1: not stored).  Returns (q_out, k_out); k_out is
     None when only the cache receives k."""
     N, Hq, Hk, d, dt = _qk_shapes(q, k)
-    dev = q.device
-    a = VdaQkArgs()
-    a.dtype = dt
-    a.q_in = _rows("q", q, q.dtype, (N, Hq, d), dev)
-    a.k_in = _rows("k", k, q.dtype, (N, Hk, d), dev)
-    a.N, a.Hq, a.Hk, a.d = N, Hq, Hk, d
-    a.q_weight = _set_weight("q_weight", q_weight, d, dev)
-    a.k_weight = _set_weight("k_weight", k_weight, d, dev)
-    _set_rotation(a, N, positions, frequencies, axis, interleaved, dev)
+    dtype, i = q.dtype, q.get_device()
+    rows_q, rows_k, rows_v, rows_ko = _rows("q", q, dtype, (N, Hq, d), i), _rows("k", k, dtype, (N, Hk, d), i), (0, 0, 0), (0, 0, 0)
+    pos, freq, ax, axes, rot = _rotation(N, positions, frequencies, axis, i)
+    at_slots = at_kc = at_vc = pages = page = 0
     if slots is not None:
-        _check_tensor("slots", slots, torch.int64, (N,), dev)
-        a.pages, a.page_size = _check_cache(k_cache, v_cache, q.dtype, Hk, d, dev)
-        a.v_in = _rows("v", v, q.dtype, (N, Hk, d), dev)
-        a.slots, a.k_cache, a.v_cache = slots.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr()
-        if N == 0:
-            a.slots = None
+        at_slots = _at("slots", slots, torch.int64, (N,), i)
+        at_kc, at_vc, pages, page = _cache(k_cache, v_cache, dtype, Hk, d, i)
+        rows_v = _rows("v", v, dtype, (N, Hk, d), i)
     elif k_cache is not None or v_cache is not None or v is not None:
         raise ValueError("v, k_cache and v_cache need slots")
     if q_out is None:
-        q_out = torch.empty((N, Hq, d), dtype=q.dtype, device=dev)
-    a.q_out = _rows("q_out", q_out, q.dtype, (N, Hq, d), dev)
+        q_out = q.new_empty((N, Hq, d))
     if k_out is None and slots is None:
-        k_out = torch.empty((N, Hk, d), dtype=q.dtype, device=dev)
+        k_out = q.new_empty((N, Hk, d))
     if k_out is not None:
-        a.k_out = _rows("k_out", k_out, q.dtype, (N, Hk, d), dev)
-    a.eps = float(eps)
-    with _on_device(dev):
-        a.stream = _stream(stream).value
-        check(lib().vda_qk_norm_rope(ctypes.byref(a)), "vda_qk_norm_rope")
+        rows_ko = _rows("k_out", k_out, dtype, (N, Hk, d), i)
+    args = _pack(
+        pack_qk, dt, *rows_q, *rows_k, *rows_v, *_rows("q_out", q_out, dtype, (N, Hq, d), i), *rows_ko,
+        _weight("q_weight", q_weight, d, i), _weight("k_weight", k_weight, d, i), pos, freq, ax,
+        at_slots, at_kc, at_vc, N, Hq, Hk, d, axes, rot, 1 if interleaved else 0, pages, page, eps,
+        _raw_stream(i, stream))
+    check(_call(i, lib().vda_qk_norm_rope, args), "vda_qk_norm_rope")
     return q_out, k_out
 
 
@@ -312,35 +323,29 @@ def vda_qk_norm_rope_backward(dq_out, dk_out, q, k, q_weight=None, k_weight=None
     inputs, returns (dq, dk, dq_weight, dk_weight); the weight gradients are
     float32 [d], sums in a fixed order (None for a weight that is None)."""
     N, Hq, Hk, d, dt = _qk_shapes(q, k)
-    dev = q.device
-    a = VdaQkGradArgs()
-    a.dtype = dt
-    a.dq_out = _rows("dq_out", dq_out, q.dtype, (N, Hq, d), dev)
-    a.dk_out = _rows("dk_out", dk_out, q.dtype, (N, Hk, d), dev)
-    a.q_in = _rows("q", q, q.dtype, (N, Hq, d), dev)
-    a.k_in = _rows("k", k, q.dtype, (N, Hk, d), dev)
-    a.N, a.Hq, a.Hk, a.d = N, Hq, Hk, d
-    a.q_weight = _set_weight("q_weight", q_weight, d, dev)
-    a.k_weight = _set_weight("k_weight", k_weight, d, dev)
-    _set_rotation(a, N, positions, frequencies, axis, interleaved, dev)
+    dtype, i = q.dtype, q.get_device()
+    pos, freq, ax, axes, rot = _rotation(N, positions, frequencies, axis, i)
     if dq is None:
-        dq = torch.empty((N, Hq, d), dtype=q.dtype, device=dev)
+        dq = q.new_empty((N, Hq, d))
     if dk is None:
-        dk = torch.empty((N, Hk, d), dtype=q.dtype, device=dev)
-    a.dq_in = _rows("dq", dq, q.dtype, (N, Hq, d), dev)
-    a.dk_in = _rows("dk", dk, q.dtype, (N, Hk, d), dev)
+        dk = q.new_empty((N, Hk, d))
+    rows = (*_rows("dq_out", dq_out, dtype, (N, Hq, d), i), *_rows("dk_out", dk_out, dtype, (N, Hk, d), i),
+            *_rows("q", q, dtype, (N, Hq, d), i), *_rows("k", k, dtype, (N, Hk, d), i),
+            *_rows("dq", dq, dtype, (N, Hq, d), i), *_rows("dk", dk, dtype, (N, Hk, d), i))
     L = lib()
-    dwq = torch.empty(d, dtype=torch.float32, device=dev) if q_weight is not None else None
-    dwk = torch.empty(d, dtype=torch.float32, device=dev) if k_weight is not None else None
-    a.dq_weight = dwq.data_ptr() if dwq is not None else None
-    a.dk_weight = dwk.data_ptr() if dwk is not None else None
-    if workspace is None and (dwq is not None or dwk is not None):
-        workspace = torch.empty(int(L.vda_qk_grad_workspace_bytes(d)), dtype=torch.uint8, device=dev)
-    a.eps = float(eps)
-    with _on_device(dev):
-        a.stream = _stream(stream).value
-        rc = L.vda_qk_norm_rope_backward(ctypes.byref(a), _ptr(workspace), 0 if workspace is None else workspace.numel())
-        check(rc, "vda_qk_norm_rope_backward")
+    dwq, dwk = torch.empty((2, d), dtype=torch.float32, device=q.device).unbind(0)
+    if q_weight is None:
+        dwq = None
+    if k_weight is None:
+        dwk = None
+    at_wq, at_wk = _weight("q_weight", q_weight, d, i), _weight("k_weight", k_weight, d, i)
+    if workspace is None and (at_wq or at_wk):
+        workspace = torch.empty(L.vda_qk_grad_workspace_bytes(d), dtype=torch.uint8, device=q.device)
+    args = _pack(
+        pack_qk_grad, dt, *rows, at_wq, at_wk, dwq.data_ptr() if at_wq else 0, dwk.data_ptr() if at_wk else 0, pos, freq, ax,
+        N, Hq, Hk, d, axes, rot, 1 if interleaved else 0, eps, _raw_stream(i, stream))
+    check(_call(i, L.vda_qk_norm_rope_backward, args, 0 if workspace is None else workspace.data_ptr(),
+                0 if workspace is None else workspace.numel()), "vda_qk_norm_rope_backward")
     return dq, dk, dwq, dwk
 
 
@@ -362,52 +367,50 @@ def vda_paged_attention(q, k_cache, v_cache, block_table, kv_len, q_start, block
     default is a new one)."""
     if q.dim() != 3:
         raise ValueError("q must be [N, Hq, d]")
-    N, Hq, d = q.shape
-    dt = _DTYPES.get(q.dtype)
+    if not q.is_cuda:
+        raise ValueError("q must be a CUDA tensor")
+    dtype, i = q.dtype, q.get_device()
+    dt = _DTYPES.get(dtype)
     if dt is None:
-        raise ValueError(f"unsupported dtype {q.dtype} (bf16 or float32)")
-    dev = q.device
+        raise ValueError(f"unsupported dtype {dtype} (bf16 or float32)")
+    N, Hq, d = q.shape
+    rows_q = _rows("q", q, dtype, (N, Hq, d), i)
     if k_cache is None or k_cache.dim() != 4:
         raise ValueError("k_cache and v_cache must be [pages, Hk, page_size, d]")
     Hk = k_cache.shape[1]
-    pages, page = _check_cache(k_cache, v_cache, q.dtype, Hk, d, dev)
+    at_kc, at_vc, pages, page = _cache(k_cache, v_cache, dtype, Hk, d, i)
     if block_table is None or block_table.dim() != 2:
         raise ValueError("block_table must be [B, max_pages]")
     B, max_pages = block_table.shape
-    if not block_table.is_cuda or block_table.device != dev or block_table.dtype != torch.int32:
-        raise ValueError(f"block_table must be int32 on {dev}")
-    if max_pages > 1 and block_table.stride(1) != 1:
+    if block_table.get_device() != i or block_table.dtype is not torch.int32:
+        raise ValueError(f"block_table must be int32 on cuda:{i}")
+    table_stride, one = block_table.stride()
+    if max_pages > 1 and one != 1:
         raise ValueError("block_table must have contiguous rows")
-    _check_tensor("kv_len", kv_len, torch.int32, (B,), dev)
-    _check_tensor("q_start", q_start, torch.int32, (B + 1,), dev)
-    a = VdaAttnArgs()
-    a.dtype = dt
-    a.q = _rows("q", q, q.dtype, (N, Hq, d), dev)
     if out is None:
-        out = torch.empty((N, Hq, d), dtype=q.dtype, device=dev)
-    a.out = _rows("out", out, q.dtype, (N, Hq, d), dev)
-    if lse is None and return_lse:
-        lse = torch.empty((N, Hq), dtype=torch.float32, device=dev)
-    if lse is not None:
-        _check_tensor("lse", lse, torch.float32, (N, Hq), dev)
-        a.lse = lse.data_ptr()
-    a.k_cache, a.v_cache = k_cache.data_ptr(), v_cache.data_ptr()
-    a.block_table, a.kv_len, a.q_start = block_table.data_ptr(), kv_len.data_ptr(), q_start.data_ptr()
-    a.table_stride = block_table.stride(0)
-    a.N, a.B, a.Hq, a.Hk, a.d = N, B, Hq, Hk, d
-    a.pages, a.page_size, a.max_pages = pages, page, max_pages
-    a.block, a.window_blocks, a.anchors = int(block), int(window_blocks), int(anchors)
-    if scale is not None:
-        a.scale = float(scale)
-        if not a.scale > 0.0:
-            raise ValueError(f"scale must be positive, got {scale}")
+        out = q.new_empty((N, Hq, d))
+    if lse is None:
+        if return_lse:
+            lse = torch.empty((N, Hq), dtype=torch.float32, device=q.device)
+            at_lse = lse.data_ptr()
+        else:
+            at_lse = 0
+    else:
+        at_lse = _at("lse", lse, torch.float32, (N, Hq), i)
+    if scale is None:
+        scale = 0.0
+    elif not scale > 0.0:
+        raise ValueError(f"scale must be positive, got {scale}")
     L = lib()
-    with _on_device(dev):
-        if workspace is None:
-            n = int(L.vda_paged_attention_workspace_bytes(dt, N, B, Hq, Hk, d, page))
-            workspace = torch.empty(n, dtype=torch.uint8, device=dev)
-        a.stream = _stream(stream).value
-        check(L.vda_paged_attention(ctypes.byref(a), _ptr(workspace), workspace.numel()), "vda_paged_attention")
+    args = _pack(
+        pack_attn, dt, *rows_q, at_kc, at_vc, block_table.data_ptr(), _at("kv_len", kv_len, torch.int32, (B,), i),
+        _at("q_start", q_start, torch.int32, (B + 1,), i), *_rows("out", out, dtype, (N, Hq, d), i), at_lse, table_stride,
+        N, B, Hq, Hk, d, pages, page, max_pages, block, window_blocks, anchors, scale,
+        _raw_stream(i, stream))
+    if workspace is None:
+        n = _call(i, L.vda_paged_attention_workspace_bytes, dt, N, B, Hq, Hk, d, page)
+        workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
+    check(_call(i, L.vda_paged_attention, args, workspace.data_ptr(), workspace.numel()), "vda_paged_attention")
     return (out, lse) if return_lse else out
 
 

@@ -6,7 +6,7 @@
 // New tokens and cached keys differ from sequence to sequence and are known
 // on the device only.  All items' key tiles, in the order sequence, KV head,
 // run of tokens, form one line of W tiles; CTA g of G takes the tiles
-// [W g / G, W (g + 1) / G), which may begin and end inside an item.  The parts
+// [W g / G, W (g + 1) / G) or so, which may begin and end inside an item.  The parts
 // of an item that several CTAs took are joined afterwards (their running
 // maximum and sum say how).  So long and short sequences, one token or
 // thousands of them, load every SM alike, without a plan made on the host.
@@ -53,9 +53,9 @@ VDA_HD Span span_of(const Geom& g, int p, int len) {
     s.end = len;
     return s;
   }
-  const long long bs = g.block;
-  const long long d = (long long)p - g.anchors;
-  const long long blk = d >= 0 ? d / bs : -((-d + bs - 1) / bs);   // floor
+  const int bs = g.block, d = p - g.anchors;
+  // floor(d / bs); block and anchors are at most 2^30
+  const long long blk = bs == 1 ? d : d >= 0 ? d / bs : -((-d + bs - 1) / bs);
   const long long e = (blk + 1) * bs + g.anchors;
   s.end = e < len ? (int)e : len;
   long long lo = g.window < 0 ? 0 : (blk - g.window) * bs + g.anchors;
@@ -105,8 +105,12 @@ VDA_HD Tiles tiles_of(const Geom& g, const Seq& s, int i0, int ntok) {
 VDA_HD int key_tile(const Tiles& t, int i) { return i < t.n_anchor ? i : t.first + (i - t.n_anchor); }
 
 // first tile of share g, and the share that holds tile x
-VDA_HD long long share_begin(long long W, int g, int G) { return W * g / G; }
-VDA_HD int share_of(long long W, long long x, int G) { return (int)(((x + 1) * G - 1) / W); }
+// (the first W % G shares have one tile more)
+VDA_HD int share_begin(int W, int g, int G) { return g * (W / G) + imin(g, W % G); }
+VDA_HD int share_of(int W, int x, int G) {
+  const int per = W / G, rem = W % G, longer = rem * (per + 1);
+  return x < longer ? x / (per + 1) : rem + (x - longer) / per;
+}
 
 // ------------------------------------------------------------------- device
 #ifdef __CUDACC__
@@ -116,16 +120,16 @@ __device__ __forceinline__ Seq load_seq(const Geom& g, int b) {
 
 // Tiles of one head of a sequence, computed by one lane.
 template <int BN>
-__device__ __forceinline__ long long seq_tiles_serial(const Geom& g, const Seq& s) {
-  long long w = 0;
+__device__ __forceinline__ int seq_tiles_serial(const Geom& g, const Seq& s) {
+  int w = 0;
   const int n = items_of(g, s.n);
   for (int r = 0; r < n; ++r) w += tiles_of<BN>(g, s, r * g.tpi, imin(g.tpi, s.n - r * g.tpi)).count;
   return w;
 }
 // ... and by a whole warp.
 template <int BN>
-__device__ __forceinline__ long long seq_tiles_warp(const Geom& g, const Seq& s, int lane) {
-  long long w = 0;
+__device__ __forceinline__ int seq_tiles_warp(const Geom& g, const Seq& s, int lane) {
+  int w = 0;
   const int n = items_of(g, s.n);
   for (int r = lane; r < n; r += 32) w += tiles_of<BN>(g, s, r * g.tpi, imin(g.tpi, s.n - r * g.tpi)).count;
 #pragma unroll
@@ -135,7 +139,7 @@ __device__ __forceinline__ long long seq_tiles_warp(const Geom& g, const Seq& s,
 
 // Where a CTA's share begins.
 struct Plan {
-  long long W, w0, w1;   // all tiles; this share
+  int W, w0, w1;         // all tiles; this share
   int shares;            // CTAs with work
   int b, h, r;           // item in which the share begins
   int t;                 // tiles of that item before it
@@ -143,13 +147,13 @@ struct Plan {
 
 constexpr int kSerialItems = 4;   // longer sequences are counted by the whole warp
 
-// All heads' tiles of sequences 32 c .. 32 c + 31, one a lane.
+// One head's tiles of sequences 32 c .. 32 c + 31, one a lane.
 template <int BN>
-__device__ __forceinline__ long long chunk_tiles(const Geom& g, int c, int lane) {
+__device__ __forceinline__ int chunk_tiles(const Geom& g, int c, int lane) {
   const int b = c * 32 + lane;
   Seq s{0, 0, 0};
   if (b < g.B) s = load_seq(g, b);
-  long long w = 0;
+  int w = 0;
   const bool longer = items_of(g, s.n) > kSerialItems;
   if (!longer) w = seq_tiles_serial<BN>(g, s);
   unsigned todo = __ballot_sync(0xffffffffu, longer);
@@ -160,19 +164,19 @@ __device__ __forceinline__ long long chunk_tiles(const Geom& g, int c, int lane)
     o.q0 = 0;
     o.n = __shfl_sync(0xffffffffu, s.n, l);
     o.len = __shfl_sync(0xffffffffu, s.len, l);
-    const long long v = seq_tiles_warp<BN>(g, o, lane);
+    const int v = seq_tiles_warp<BN>(g, o, lane);
     if (lane == l) w = v;
   }
-  return w * g.Hk;
+  return w;
 }
 
-// One warp finds share `cta` of `ctas` (no share below min_tiles tiles while
-// there is more than one).  The first kKeep chunks of 32 sequences are
-// counted once and kept in registers.
+// One warp finds share `cta` of `ctas`.  The first kKeep chunks of 32
+// sequences are counted once and kept in registers.  The host bounds W for
+// ascending q_start; sequences that overlap so that W passes 2^31 get nothing.
 template <int BN>
-__device__ __forceinline__ Plan plan_share(const Geom& g, int cta, int ctas, int min_tiles, int lane) {
+__device__ __forceinline__ Plan plan_share(const Geom& g, int cta, int ctas, int lane) {
   constexpr int kKeep = 4;
-  long long keep[kKeep];
+  int keep[kKeep];
   long long total = 0;
   const int chunks = (g.B + 31) / 32;
 #pragma unroll
@@ -180,23 +184,22 @@ __device__ __forceinline__ Plan plan_share(const Geom& g, int cta, int ctas, int
     keep[c] = c < chunks ? chunk_tiles<BN>(g, c, lane) : 0;
     total += keep[c];
   }
+#pragma unroll 1
   for (int c = kKeep; c < chunks; ++c) total += chunk_tiles<BN>(g, c, lane);
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) total += __shfl_xor_sync(0xffffffffu, total, off);
+  total *= g.Hk;
   Plan p;
-  p.W = total;
-  p.b = p.h = p.r = p.t = 0;
-  const long long most = total / min_tiles;
-  p.shares = total == 0 ? 0 : (int)(most < 1 ? 1 : (most < ctas ? most : ctas));
-  if (cta >= p.shares) {
-    p.w0 = p.w1 = 0;
-    return p;
-  }
-  p.w0 = share_begin(total, cta, p.shares);
-  p.w1 = share_begin(total, cta + 1, p.shares);
-  long long before = 0;
+  p.W = total > 2147483647LL ? 0 : (int)total;
+  p.w0 = p.w1 = p.b = p.h = p.r = p.t = 0;
+  p.shares = imin(p.W, ctas);
+  if (cta >= p.shares) return p;
+  p.w0 = share_begin(p.W, cta, p.shares);
+  p.w1 = share_begin(p.W, cta + 1, p.shares);
+  int rest = p.w0;   // tiles still to pass
+#pragma unroll 1
   for (int c = 0; c < chunks; ++c) {
-    long long w = 0;
+    int w = 0;
     if (c < kKeep) {
 #pragma unroll
       for (int k = 0; k < kKeep; ++k)
@@ -204,44 +207,46 @@ __device__ __forceinline__ Plan plan_share(const Geom& g, int cta, int ctas, int
     } else {
       w = chunk_tiles<BN>(g, c, lane);
     }
-    long long upto = w;   // inclusive prefix over the lanes
+    int upto = w * g.Hk;   // inclusive prefix over the lanes
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
-      const long long v = __shfl_up_sync(0xffffffffu, upto, off);
+      const int v = __shfl_up_sync(0xffffffffu, upto, off);
       if (lane >= off) upto += v;
     }
-    const unsigned hit = __ballot_sync(0xffffffffu, before + upto > p.w0);
-    if (hit) {
-      const int l = __ffs(hit) - 1;
-      const long long wl = __shfl_sync(0xffffffffu, w, l);
-      long long rest = p.w0 - before - (__shfl_sync(0xffffffffu, upto, l) - wl);
-      p.b = c * 32 + l;
-      const long long per_head = wl / g.Hk;
-      p.h = (int)(rest / per_head);
-      rest -= p.h * per_head;
-      // the run of tokens that holds tile `rest` of this head
-      const Seq s = load_seq(g, p.b);
-      const int n = items_of(g, s.n);
-      for (int r0 = 0; r0 < n; r0 += 32) {
-        const int r = r0 + lane;
-        long long k = r < n ? tiles_of<BN>(g, s, r * g.tpi, imin(g.tpi, s.n - r * g.tpi)).count : 0, pre = k;
-#pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-          const long long v = __shfl_up_sync(0xffffffffu, pre, off);
-          if (lane >= off) pre += v;
-        }
-        const unsigned at = __ballot_sync(0xffffffffu, pre > rest);
-        if (at) {
-          const int rl = __ffs(at) - 1;
-          p.r = r0 + rl;
-          p.t = (int)(rest - (__shfl_sync(0xffffffffu, pre, rl) - __shfl_sync(0xffffffffu, k, rl)));
-          break;
-        }
-        rest -= __shfl_sync(0xffffffffu, pre, 31);
-      }
-      break;
+    const unsigned hit = __ballot_sync(0xffffffffu, upto > rest);
+    if (!hit) {
+      rest -= __shfl_sync(0xffffffffu, upto, 31);
+      continue;
     }
-    before += __shfl_sync(0xffffffffu, upto, 31);
+    const int l = __ffs(hit) - 1;
+    const int per_head = __shfl_sync(0xffffffffu, w, l);
+    rest -= __shfl_sync(0xffffffffu, upto, l) - per_head * g.Hk;
+    p.b = c * 32 + l;
+    p.h = rest / per_head;
+    rest -= p.h * per_head;
+    // the run of tokens that holds tile `rest` of this head
+    const Seq s = load_seq(g, p.b);
+    const int n = items_of(g, s.n);
+#pragma unroll 1
+    for (int r0 = 0; r0 < n; r0 += 32) {
+      const int r = r0 + lane;
+      const int k = r < n ? tiles_of<BN>(g, s, r * g.tpi, imin(g.tpi, s.n - r * g.tpi)).count : 0;
+      int pre = k;
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, pre, off);
+        if (lane >= off) pre += v;
+      }
+      const unsigned at = __ballot_sync(0xffffffffu, pre > rest);
+      if (at) {
+        const int rl = __ffs(at) - 1;
+        p.r = r0 + rl;
+        p.t = rest - (__shfl_sync(0xffffffffu, pre, rl) - __shfl_sync(0xffffffffu, k, rl));
+        break;
+      }
+      rest -= __shfl_sync(0xffffffffu, pre, 31);
+    }
+    break;
   }
   return p;
 }
@@ -251,7 +256,7 @@ __device__ __forceinline__ Plan plan_share(const Geom& g, int cta, int ctas, int
 template <int BN>
 struct Walk {
   const Geom* g;
-  long long left;        // tiles of the share from this item's on
+  int left;              // tiles of the share from this item's on
   int b, h, r;
   Seq s;
   int i0, ntok;          // tokens [i0, i0 + ntok) of the sequence
@@ -270,7 +275,7 @@ struct Walk {
     i0 = r * g->tpi;
     ntok = imin(g->tpi, s.n - i0);
     tiles = tiles_of<BN>(*g, s, i0, ntok);
-    t1 = left < tiles.count - t0 ? t0 + (int)left : tiles.count;
+    t1 = left < tiles.count - t0 ? t0 + left : tiles.count;
   }
   __device__ __forceinline__ int n() const { return t1 - t0; }
   __device__ __forceinline__ bool whole() const { return t0 == 0 && t1 == tiles.count; }

@@ -96,7 +96,7 @@ k_attn_simt(const T* __restrict__ q, int64_t q_ts, int64_t q_hs, const T* __rest
   ptx::grid_wait_prerequisites();
   ptx::grid_launch_dependents();
   if (tid < 32) {
-    const Plan p = plan_share<BN>(g, blockIdx.x, gridDim.x, 1, tid);
+    const Plan p = plan_share<BN>(g, blockIdx.x, gridDim.x, tid);
     if (tid == 0) *plan = p;
   }
   __syncthreads();
@@ -222,7 +222,7 @@ k_attn_simt(const T* __restrict__ q, int64_t q_ts, int64_t q_hs, const T* __rest
     const bool whole = w.whole();
     const int slot = w.t0 > 0 ? 0 : 1;
     if (!whole && slot == 1) {   // begun here, continued in later shares
-      const long long start = pl.w1 - w.n();
+      const int start = pl.w1 - w.n();
       meta.parts = share_of(pl.W, start + w.tiles.count - 1, pl.shares) - (int)blockIdx.x + 1;
       meta.tok0 = tok0;
       meta.h = w.h;
@@ -273,27 +273,52 @@ k_attn_join(Parts parts, OutView<T> ov, int group) {
     auto row = [&](int i) -> size_t {
       return (((size_t)blockIdx.x + i) * 2 + (i == 0 ? 1 : 0)) * parts.rows + r;
     };
-    float m = neg_inf();
-    for (int i = 0; i < me.parts; ++i) m = fmaxf(m, parts.ml[row(i)].x);
-    const float base = m == neg_inf() ? 0.f : m;
-    float l = 0.f, o[CPL];
+    // lane i holds the maximum and sum of part i (of 32 at a time)
+    float m = neg_inf(), l = 0.f, o[CPL];
 #pragma unroll
     for (int c = 0; c < CPL; ++c) o[c] = 0.f;
-    for (int i = 0; i < me.parts; ++i) {
-      const size_t at = row(i);
-      const float2 ml = parts.ml[at];
-      const float a = exp2f(ml.x - base);
-      l = fmaf(ml.y, a, l);
+    for (int i0 = 0; i0 < me.parts; i0 += 32) {
+      const int n = imin(32, me.parts - i0);
+      const float2 ml = lane < n ? parts.ml[row(i0 + lane)] : make_float2(neg_inf(), 0.f);
+      float mn = fmaxf(m, ml.x);
 #pragma unroll
-      for (int c = 0; c < CPL; ++c)
-        if (c * 32 + lane < D) o[c] = fmaf(parts.o[at * D + c * 32 + lane], a, o[c]);
+      for (int off = 16; off > 0; off >>= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, off));
+      const float base = mn == neg_inf() ? 0.f : mn;
+      const float before = exp2f(m - base), a = exp2f(ml.x - base);
+      float sum = ml.y * a;
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+      l = fmaf(l, before, sum);
+      m = mn;
+#pragma unroll
+      for (int c = 0; c < CPL; ++c) o[c] *= before;
+#pragma unroll 8
+      for (int i = 0; i < n; ++i) {
+        const float ai = __shfl_sync(0xffffffffu, a, i);
+        const float* src = parts.o + row(i0 + i) * D + lane * CPL;
+        if constexpr (CPL == 4) {
+          const float4 x = *reinterpret_cast<const float4*>(src);
+          o[0] = fmaf(x.x, ai, o[0]); o[1] = fmaf(x.y, ai, o[1]);
+          o[2] = fmaf(x.z, ai, o[2]); o[3] = fmaf(x.w, ai, o[3]);
+        } else {
+#pragma unroll
+          for (int c = 0; c < CPL; ++c)
+            if (lane * CPL + c < D) o[c] = fmaf(src[c], ai, o[c]);
+        }
+      }
     }
     const float inv = l == 0.f ? 0.f : 1.f / l;
     const int tok = me.tok0 + r / group, hd = me.h * group + r % group;
-    T* dst = ov.out + (int64_t)tok * ov.ts + (int64_t)hd * ov.hs;
+    T* dst = ov.out + (int64_t)tok * ov.ts + (int64_t)hd * ov.hs + lane * CPL;
 #pragma unroll
-    for (int c = 0; c < CPL; ++c)
-      if (c * 32 + lane < D) dst[c * 32 + lane] = from_f32<T>(o[c] * inv);
+    for (int c = 0; c < CPL; ++c) o[c] *= inv;
+    if constexpr (CPL == 4) {
+      store4(dst, make_float4(o[0], o[1], o[2], o[3]));
+    } else {
+#pragma unroll
+      for (int c = 0; c < CPL; ++c)
+        if (lane * CPL + c < D) dst[c] = from_f32<T>(o[c]);
+    }
     if (lane == 0 && ov.lse) ov.lse[(int64_t)tok * ov.Hq + hd] = l == 0.f ? neg_inf() : (m + log2f(l)) * kLn2;
   }
 }
@@ -304,6 +329,7 @@ inline size_t align256(size_t x) { return (x + 255) / 256 * 256; }
 struct AttnPlan {
   bool tc;
   int ctas, rows, tpi;     // CTAs, rows of a part, tokens of an item
+  int join_y;              // blocks of eight rows at a time that join one item
   size_t off_ml, off_meta, total;
 };
 
@@ -329,6 +355,9 @@ inline AttnPlan make_attn_plan(int dtype, int Hq, int Hk, int d, int page, long 
     p.ctas = 2 * sms;
     p.tpi = p.rows / G;
   }
+  // rows that an item has on average
+  const long long per = N * G / (B > 0 ? B : 1) + 1;
+  p.join_y = (int)((per < p.rows ? per : p.rows) + 15) / 16;
   const size_t slots = (size_t)p.ctas * 2 * p.rows;
   p.off_ml = align256(slots * d * sizeof(float));
   p.off_meta = p.off_ml + align256(slots * sizeof(float2));
@@ -361,7 +390,7 @@ inline Parts parts_of(char* ws, const AttnPlan& p) {
 
 template <typename T, int D>
 int launch_join(const AttnPlan& p, const Parts& parts, const OutView<T>& ov, int group, cudaStream_t s) {
-  return tc::launch_pdl("k_attn_join", k_attn_join<T, D>, dim3((unsigned)p.ctas, (unsigned)(p.rows / 16)), dim3(256), 0, s,
+  return tc::launch_pdl("k_attn_join", k_attn_join<T, D>, dim3((unsigned)p.ctas, (unsigned)p.join_y), dim3(256), 0, s,
                         parts, ov, group);
 }
 

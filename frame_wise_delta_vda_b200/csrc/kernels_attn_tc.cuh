@@ -16,8 +16,7 @@
 // so the output in TMEM is rarely scaled.
 //
 // Warps 0-3 and 4-7: softmax and output of turn 0 and 1; warp 8: K, V loads;
-// warp 9: MMA; warp 10: Q loads; warp 11 completes the warpgroup whose
-// registers go to the softmax warps.
+// warps 9 and 10: MMA of turn 0 and 1; warp 11: the list of items and Q loads.
 #pragma once
 
 #include "kernels_attn.cuh"
@@ -26,16 +25,40 @@
 namespace vda {
 namespace attn {
 
-// D[tmem] (+)= A[tmem] * B[smem desc], kind::f16: A is 128 lanes x 8 columns of
-// bf16 pairs (K-major).
-__device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
-                                            uint32_t accumulate) {
+// Matrix descriptors as 32-bit halves, so that the addresses of a product's
+// steps are one 32-bit add each: the high half holds SBO = 1024, version 1 and
+// the 128-B swizzle (see ptx::desc_sw128), the low half address and LBO.
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lbo) {
+  return ((saddr & 0x3FFFFu) >> 4) | ((lbo >> 4) << 16);
+}
+// D[tmem] (+)= A[smem] * B[smem], kind::f16
+__device__ __forceinline__ void mma_ss(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
-      ::"r"(d_tmem), "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+      "setp.ne.b32 p, %5, 0;\n\t"
+      "mov.b64 a, {%1, %3};\n\t"
+      "mov.b64 b, {%2, %3};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;\n\t}"
+      ::"r"(d_tmem), "r"(a_lo), "r"(b_lo), "r"(kDescHi), "r"(idesc), "r"(accumulate)
       : "memory");
+}
+// D[tmem] (+)= A[tmem] * B[smem], kind::f16: A is 128 lanes x 8 columns of
+// bf16 pairs (K-major).
+__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\t"
+      "setp.ne.b32 p, %5, 0;\n\t"
+      "mov.b64 b, {%2, %3};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t}"
+      ::"r"(d_tmem), "r"(a_tmem), "r"(b_lo), "r"(kDescHi), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// True for one lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.b32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
 }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -59,6 +82,33 @@ __device__ __forceinline__ uint32_t absent_word(uint32_t absent, int c, int box)
   return w;
 }
 
+// ptx::mbar_wait by a whole converged warp, with one answer for all lanes; a
+// phase that is over already costs one poll and one vote.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort) {
+  if (__all_sync(0xffffffffu, ptx::mbar_try_wait(bar, parity))) return true;
+  return __all_sync(0xffffffffu, ptx::mbar_wait(bar, parity, abort));
+}
+// A count in shared memory that several warps add to (release) and one waits
+// for (acquire), with the bounds of ptx::mbar_wait: for a waiter that does not
+// see every phase, where a barrier's parity would be ambiguous.
+__device__ __forceinline__ void count_add(uint32_t* c) {
+  asm volatile("red.release.cta.shared::cta.add.u32 [%0], 1;" ::"r"(ptx::smem_u32(c)) : "memory");
+}
+__device__ __forceinline__ bool count_wait(const uint32_t* c, uint32_t n, volatile int* abort) {
+  const long long t0 = clock64();
+  while (true) {
+    uint32_t v;
+    asm volatile("ld.acquire.cta.shared::cta.u32 %0, [%1];" : "=r"(v) : "r"(ptx::smem_u32(c)) : "memory");
+    if (v >= n) return true;
+    if (*abort) return false;
+    if (clock64() - t0 > ptx::kWaitCycles) {
+      raise_device_error(kErrWaitTimeout);
+      *abort = 1;
+      return false;
+    }
+  }
+}
+
 template <int D>
 struct TcCfg {
   static constexpr int BN = 128;                       // keys of a tile
@@ -67,48 +117,42 @@ struct TcCfg {
   static constexpr uint32_t BLK = 128 * 128;           // 128 rows x 64 bf16
   static constexpr uint32_t TILE = NB * BLK;
   static constexpr int NST = D == 128 ? 5 : 10;        // K / V stages
+  static constexpr int NIT = 4;                        // items ahead
+  static constexpr int NGONE = 16;                     // key tiles whose absent pages are kept (> NST / 2 + 1)
   static constexpr uint32_t OFF_Q = 0;                 // two row tiles; the second is also the merge's buffer
   static constexpr uint32_t OFF_KV = 2 * TILE;
   static constexpr uint32_t OFF_ML = OFF_KV + NST * TILE;   // merge: 64 rows x (m, l)
-  static constexpr uint32_t OFF_BAR = OFF_ML + 64 * 8;
-  // kvfull[NST], kvempty[NST], qfull, qempty, sfull[2], pfull[2], odone[2], ofree[2], handed, merged, drain
-  static constexpr int NBAR = 2 * NST + 13;
-  static constexpr uint32_t OFF_PLAN = OFF_BAR + NBAR * 8 + 16;
-  static constexpr size_t SMEM = OFF_PLAN + sizeof(Plan) + 1024;
-  static constexpr int WARP_KV = 8, WARP_MMA = 9, WARP_Q = 10, THREADS = 384;
-  // registers: 384 threads x 168 at launch = 64512 >= 256 x 208 + 128 x 80 after the split
-  static constexpr int REG_SOFTMAX = 208, REG_OTHER = 80;
-  // TMEM columns: S (P over its first half) of turn 0, 1; output of turn 0, 1
+  static constexpr uint32_t OFF_ITEM = OFF_ML + 64 * 8;
+  static constexpr uint32_t OFF_GONE = OFF_ITEM + NIT * 64;
+  static constexpr uint32_t OFF_BAR = OFF_GONE + NGONE * 4;
+  // kvfull[NST], kvempty[NST], itfull[NIT], itempty[NIT], qfull, qempty, sfull[2][2], pfull[2][2], odone[2][2], ofree[2],
+  // handed, merged, drain[2], exped[2][4]
+  static constexpr int NBAR = 2 * NST + 2 * NIT + 28;
+  static constexpr size_t SMEM = OFF_BAR + NBAR * 8 + 16 + 1024;   // + TMEM address, abort flag, merge count
+  static constexpr int WARP_KV = 8, WARP_MMA = 9, WARP_ITEM = 11, THREADS = 384;
+  // registers: 384 threads x 168 at launch = 64512 >= 256 x 200 + 128 x 96 after the split
+  static constexpr int REG_SOFTMAX = 200, REG_OTHER = 96;
+  // TMEM columns: S of turn 0, 1, each in halves of 64 keys (a half's P over its
+  // first 32 columns); output of turn 0, 1
   static constexpr uint32_t T_S = 0, T_O = 256, T_COLS = 512;
 };
 
-// The turns of an item: a unit is one key tile of one row tile.
-template <int BN>
-struct Units {
-  Walk<BN> w;
-  int u, nu;       // unit of the item, units
-  int items;       // items before this one
-  int base;        // key tiles of earlier items of this share
-  __device__ __forceinline__ Units(const Geom& g, const Plan& p) : w(g, p), u(0), items(0), base(0) { size(); }
-  // an item with at most half its tokens has one row tile
-  __device__ __forceinline__ bool single() const { return 2 * w.ntok <= w.g->tpi; }
-  // 64-row halves of a single tile whose two turns are merged
-  __device__ __forceinline__ int halves() const {
-    return !single() || w.n() < 2 ? 0 : w.ntok * w.g->group > 64 ? 2 : 1;
-  }
-  __device__ __forceinline__ void size() { nu = !w.live ? 0 : single() ? w.n() : 2 * w.n(); }
-  __device__ __forceinline__ int turn() const { return u & 1; }
-  __device__ __forceinline__ int tile() const { return single() ? u : u >> 1; }
-  __device__ __forceinline__ bool tile_ends() const { return single() || (u & 1); }
-  __device__ __forceinline__ void next() {
-    if (++u < nu) return;
-    u = 0;
-    base += w.n();
-    ++items;
-    w.next();
-    size();
-  }
+// One item of this CTA's share, published in shared memory by the item warp.
+struct Item {
+  int b, h;              // sequence, KV head
+  int tok0, ntok;        // first token of the batch, tokens
+  int pos0, len;         // position of the first token, keys of the sequence
+  int lo, end, anc;      // keys that any of its rows sees: [lo, end) and [0, anc)
+  int n_anchor, first;   // see Tiles
+  int t0, n;             // this share's key tiles of the item; n = 0 ends the list
+  int flags;
+  int pad[2];
 };
+static_assert(sizeof(Item) == 64, "ring stride");
+constexpr int kSingle = 1;     // one row tile: the turns alternate over the key tiles
+constexpr int kWhole = 2;      // no other share has a part of it
+constexpr int kLast = 4;       // continued in later shares: part slot 1
+constexpr int kHalfShift = 4;  // 64-row halves that the turns' merge takes (0-2)
 
 template <int D>
 __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
@@ -122,241 +166,409 @@ k_attn_tc(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUten
   uint8_t* smem = tc::align1024(smem_raw);
   const uint32_t sbase = smem_u32(smem);
   auto BAR = [&](int i) -> uint32_t { return sbase + C::OFF_BAR + 8u * (uint32_t)i; };
-  constexpr int KVFULL = 0, KVEMPTY = C::NST, QFULL = 2 * C::NST, QEMPTY = QFULL + 1, SFULL = QFULL + 2, PFULL = SFULL + 2,
-                ODONE = PFULL + 2, OFREE = ODONE + 2, HANDED = OFREE + 2, MERGED = HANDED + 1, DRAIN = MERGED + 1;
+  constexpr int KVFULL = 0, KVEMPTY = C::NST, ITFULL = 2 * C::NST, ITEMPTY = ITFULL + C::NIT, QFULL = ITEMPTY + C::NIT,
+                QEMPTY = QFULL + 1, SFULL = QFULL + 2, PFULL = SFULL + 4, ODONE = PFULL + 4, OFREE = ODONE + 4,
+                HANDED = OFREE + 2, MERGED = HANDED + 1, DRAIN = MERGED + 1,
+                EXPED = DRAIN + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_BAR + C::NBAR * 8);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  Plan* splan = reinterpret_cast<Plan*>(smem + C::OFF_PLAN);
+  volatile Item* items = reinterpret_cast<volatile Item*>(smem + C::OFF_ITEM);
+  uint32_t* merged = tmem_slot + 2;   // 64-row halves of merges that are read, times four warps
+  volatile uint32_t* gone = reinterpret_cast<volatile uint32_t*>(smem + C::OFF_GONE);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
     for (int s = 0; s < C::NST; ++s) {
       mbar_init(BAR(KVFULL + s), 1);
-      mbar_init(BAR(KVEMPTY + s), 1);
+      mbar_init(BAR(KVEMPTY + s), 2);    // both MMA warps
+    }
+    for (int s = 0; s < C::NIT; ++s) {
+      mbar_init(BAR(ITFULL + s), 1);
+      mbar_init(BAR(ITEMPTY + s), 11);   // eight softmax warps, K/V, two MMA
     }
     mbar_init(BAR(QFULL), 1);
-    mbar_init(BAR(QEMPTY), 1);
+    mbar_init(BAR(QEMPTY), 2);
     for (int s = 0; s < 2; ++s) {
-      mbar_init(BAR(SFULL + s), 1);
-      mbar_init(BAR(PFULL + s), 128);
-      mbar_init(BAR(ODONE + s), 1);
-      mbar_init(BAR(OFREE + s), 128);
+      mbar_init(BAR(SFULL + 2 * s), 1);
+      mbar_init(BAR(SFULL + 2 * s + 1), 1);
+      mbar_init(BAR(PFULL + 2 * s), 4);
+      mbar_init(BAR(PFULL + 2 * s + 1), 4);
+      mbar_init(BAR(ODONE + 2 * s), 1);
+      mbar_init(BAR(ODONE + 2 * s + 1), 1);
+      mbar_init(BAR(OFREE + s), 4);
     }
-    mbar_init(BAR(HANDED), 128);
-    mbar_init(BAR(MERGED), 128);
+    mbar_init(BAR(HANDED), 4);
+    mbar_init(BAR(MERGED), 4);
     mbar_init(BAR(DRAIN), 1);
+    mbar_init(BAR(DRAIN + 1), 1);
+    for (int s = 0; s < 8; ++s) mbar_init(BAR(EXPED + s), 1);
     *abort_flag = 0;
+    *merged = 0u;
     fence_mbar_init();
   }
   if (warp == C::WARP_MMA) {
     tmem_alloc(smem_u32(tmem_slot), C::T_COLS);
     tmem_relinquish();
   }
-  grid_wait_prerequisites();
-  grid_launch_dependents();
-  if (warp == 0) {
-    const Plan p = plan_share<BN>(g, blockIdx.x, gridDim.x, 1, lane);
-    if (lane == 0) *splan = p;
-  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  grid_wait_prerequisites();
+  grid_launch_dependents();
   const uint32_t tmem = *tmem_slot;
-  const Plan plan = *splan;
   const int tpt = g.tpi >> 1;   // tokens of a row tile
+  // A barrier's parity tells a phase only from the one before and the one after
+  // it, so every waiter here either sees each phase in its turn (and the
+  // phase after it cannot end before the waiter's own arrival), or waits for a
+  // phase whose predecessor a barrier that it has passed implies.
+  // wait for item i of the share; the same for a whole warp
+  auto item_ready = [&](int i) -> bool {
+    return mbar_wait(BAR(ITFULL + i % C::NIT), (uint32_t)(i / C::NIT) & 1u, abort_flag);
+  };
 
   if (warp >= C::WARP_KV) {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::REG_OTHER));
-  if (warp == C::WARP_KV) {
-    // ---------------- K and V tiles, page by page: lane i sends page i of the tile
-    const int box = cv.page < BN ? cv.page : BN, boxes = BN / box;
-    uint32_t idx = 0, sent = 0;
-    bool ok = true;
-    for (Walk<BN> w(g, plan); ok && w.live; w.next()) {
-      for (int t = w.t0; t < w.t1; ++t, idx += 2) {
-        const int j = key_tile(w.tiles, t) * BN + lane * box;
-        // pages that no row of the item sees, or that do not exist, load as
-        // zeros: their coordinate lies outside the map
-        int row = -1;
-        if (lane < boxes && ((j < w.tiles.anc) || (j < w.tiles.end && j + box > w.tiles.lo))) {
-          const int id = __ldg(cv.table + (int64_t)w.b * cv.table_stride + j / cv.page);
-          if (id >= 0 && id < cv.pages) row = id * g.Hk + w.h;
-        }
-#pragma unroll
-        for (int v = 0; v < 2; ++v) {
-          const uint32_t s = (idx + v) % C::NST, ph = ((idx + v) / C::NST) & 1u;
-          if (!__all_sync(0xffffffffu, mbar_wait(BAR(KVEMPTY + s), ph ^ 1u, abort_flag))) { ok = false; break; }
-          if (lane == 0) mbar_arrive_expect_tx(BAR(KVFULL + s), C::TILE);
-          __syncwarp();
-          if (lane < boxes) {
-            const uint32_t dst = sbase + C::OFF_KV + s * C::TILE + (uint32_t)(lane * box) * 128u;
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::REG_OTHER));
+    if (warp == C::WARP_ITEM) {
+      // ---------------- the share's items, published one ahead of their Q tiles
+      const Plan plan = plan_share<BN>(g, blockIdx.x, gridDim.x, lane);
+      if (lane == 0) {
+        Meta meta{0, 0, 0, 0};
+        Walk<BN> w(g, plan);
+        auto publish = [&](int i) -> bool {
+          const int s = i % C::NIT;
+          if (!mbar_wait(BAR(ITEMPTY + s), ((uint32_t)(i / C::NIT) & 1u) ^ 1u, abort_flag)) return false;
+          volatile Item& it = items[s];
+          it.n = w.live ? w.n() : 0;
+          if (w.live) {
+            const bool single = 2 * w.ntok <= g.tpi, last = !w.whole() && w.t0 == 0;
+            const int rows = w.ntok * g.group;
+            it.b = w.b;
+            it.h = w.h;
+            it.tok0 = w.s.q0 + w.i0;
+            it.ntok = w.ntok;
+            it.pos0 = w.s.len - w.s.n + w.i0;
+            it.len = w.s.len;
+            it.lo = w.tiles.lo;
+            it.end = w.tiles.end;
+            it.anc = w.tiles.anc;
+            it.n_anchor = w.tiles.n_anchor;
+            it.first = w.tiles.first;
+            it.t0 = w.t0;
+            it.flags = (single ? kSingle : 0) | (w.whole() ? kWhole : 0) | (last ? kLast : 0) |
+                       ((single && w.n() > 1 ? (rows > 64 ? 2 : 1) : 0) << kHalfShift);
+            if (last) {
+              meta.parts = share_of(plan.W, plan.w1 - w.n() + w.tiles.count - 1, plan.shares) - (int)blockIdx.x + 1;
+              meta.tok0 = w.s.q0 + w.i0;
+              meta.h = w.h;
+              meta.rows = rows;
+            }
+          }
+          mbar_arrive(BAR(ITFULL + s));
+          if (w.live) w.next();
+          return true;
+        };
+        int merges = 0, sent = 0;
+        bool ok = publish(0);
+        for (int i = 0; ok && items[i % C::NIT].n != 0; ++i) {
+          const volatile Item& it = items[i % C::NIT];   // its place is not used again before item i + NIT
+          if (!publish(i + 1)) break;
+          const int flags = it.flags, h = it.h, tok0 = it.tok0;
+          const bool one = flags & kSingle;
+          if (!mbar_wait(BAR(QEMPTY), (uint32_t)(i & 1) ^ 1u, abort_flag)) break;
+          // the second tile's place has been the buffer of the last merge
+          if (!one && !count_wait(merged, 4u * (uint32_t)merges, abort_flag)) break;
+          const uint32_t bytes = (uint32_t)(tpt * g.group) * 128u * C::NB;
+          mbar_arrive_expect_tx(BAR(QFULL), one ? bytes : 2 * bytes);
+          for (int s = 0; s < (one ? 1 : 2); ++s)
 #pragma unroll
             for (int cb = 0; cb < C::NB; ++cb)
-              tma_load_3d(dst + cb * C::BLK, v ? &tmV : &tmK, 64 * cb, j % cv.page, row, BAR(KVFULL + s));
+              tma_load_3d(sbase + C::OFF_Q + s * C::TILE + cb * C::BLK, &tmQ, 64 * cb, h * g.group, tok0 + s * tpt, BAR(QFULL));
+          ++sent;
+          merges += flags >> kHalfShift;
+        }
+        if (*abort_flag && sent > 0) mbar_wait_drain(BAR(QFULL), (uint32_t)(sent - 1) & 1u);
+        parts.meta[blockIdx.x] = meta;
+      }
+      __syncwarp();
+    } else if (warp == C::WARP_KV) {
+      // ---------------- K and V tiles, page by page: lane i sends page i of the tile
+      const int box = cv.page < BN ? cv.page : BN, boxes = BN / box;
+      uint32_t idx = 0, sent = 0;
+      bool ok = true;
+      for (int i = 0; ok; ++i) {
+        if (!__all_sync(0xffffffffu, item_ready(i))) break;
+        const volatile Item& it = items[i % C::NIT];
+        const int n = it.n;
+        if (n == 0) break;
+        const int lo = it.lo, end = it.end, anc = it.anc, n_anchor = it.n_anchor, first = it.first, t0 = it.t0, h = it.h;
+        const int* row_of = cv.table + (int64_t)it.b * cv.table_stride;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(BAR(ITEMPTY + i % C::NIT));
+        // pages that no row of the item sees, or that do not exist, load as
+        // zeros: their coordinate lies outside the map.  -1: such a page,
+        // -2: one that is seen but does not exist.
+        auto page_row = [&](int t) -> int {
+          const int kt = t < n_anchor ? t : first + (t - n_anchor), j = kt * BN + lane * box;
+          if (lane >= boxes || !(j < anc || (j < end && j + box > lo))) return -1;
+          const int id = __ldg(row_of + j / cv.page);
+          return id >= 0 && id < cv.pages ? id * g.Hk + h : -2;
+        };
+        int row = page_row(t0);
+        for (int t = 0; t < n; ++t, idx += 2) {
+          const int here = row;
+          if (t + 1 < n) row = page_row(t0 + t + 1);
+          const int kt = t0 + t < n_anchor ? t0 + t : first + (t0 + t - n_anchor);
+          const int off = (kt * BN + lane * box) % cv.page;
+          const uint32_t absent = __ballot_sync(0xffffffffu, here == -2);
+#pragma unroll
+          for (int v = 0; v < 2; ++v) {
+            const uint32_t s = (idx + v) % C::NST, ph = ((idx + v) / C::NST) & 1u;
+            if (!warp_wait(BAR(KVEMPTY + s), ph ^ 1u, abort_flag)) { ok = false; break; }
+            if (lane == 0) {
+              if (v == 0) gone[(idx >> 1) % C::NGONE] = absent;
+              mbar_arrive_expect_tx(BAR(KVFULL + s), C::TILE);
+            }
+            __syncwarp();
+            if (lane < boxes) {
+              const uint32_t dst = sbase + C::OFF_KV + s * C::TILE + (uint32_t)(lane * box) * 128u;
+#pragma unroll
+              for (int cb = 0; cb < C::NB; ++cb)
+                tma_load_3d(dst + cb * C::BLK, v ? &tmV : &tmK, 64 * cb, off, here < 0 ? -1 : here, BAR(KVFULL + s));
+            }
+            __syncwarp();
+            ++sent;
+          }
+          if (!ok) break;
+        }
+      }
+      if (*abort_flag && lane == 0) {   // let issued copies land
+        const uint32_t n = sent < (uint32_t)C::NST ? sent : (uint32_t)C::NST;
+        for (uint32_t k = sent - n; k < sent; ++k) mbar_wait_drain(BAR(KVFULL + k % C::NST), (k / C::NST) & 1u);
+      }
+      __syncwarp();
+    } else {
+      // ---------------- MMA issuers, one warp a turn.  A key tile's scores are
+      // taken in halves of 64 keys, so that one half's are computed while the
+      // softmax works on the other: P V of a half, then the next tile's scores
+      // into its place.  An issuing warp spends as long again on waits and
+      // commits as its products take; two of them fill each other's gaps (one
+      // warp for both turns kept the tensor cores busy 45% of the time).  The
+      // whole warp walks the units, so that addresses stay in uniform
+      // registers, and one lane issues.
+      constexpr uint32_t kIdQK = idesc_bf16(128, 64, 0, 0);   // both K-major
+      constexpr uint32_t kIdPV = idesc_bf16(128, D, 0, 1);    // V: channels contiguous
+      const int tn = __shfl_sync(0xffffffffu, warp, 0) - C::WARP_MMA;
+      const uint32_t k_lo = desc_lo(sbase + C::OFF_KV, 16), v_lo = desc_lo(sbase + C::OFF_KV, C::BLK);
+      const uint32_t tS = tmem + C::T_S + (uint32_t)tn * 128u, tO = tmem + C::T_O + (uint32_t)(tn * D);
+      const bool leader = elect_one();
+      auto wait = [&](int bar, uint32_t parity) -> bool {
+        return warp_wait(BAR(bar), parity & 1u, abort_flag);
+      };
+      uint32_t stage = 0, phase = 0;      // of the next K or V
+      uint32_t units = 0, begun = 0;      // of this turn: units with V's product issued; items begun
+      bool ok = true;
+      auto advance = [&]() {
+        if (++stage == C::NST) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      };
+      // the unit whose scores are issued and whose product with V is not
+      bool due = false, due_first = false;
+      uint32_t due_stage = 0, due_phase = 0;
+      auto pv = [&](int half) -> bool {
+        if (half == 0) {
+          if (!wait(KVFULL + due_stage, due_phase)) return false;
+          if (due_first && !wait(OFREE + tn, begun++ ^ 1u)) return false;   // the output of the last item has been read
+        }
+        if (!wait(PFULL + 2 * tn + half, units)) return false;
+        tc_fence_after();
+        if (leader) {
+          const uint32_t vb = v_lo + due_stage * (C::TILE >> 4) + (uint32_t)half * (4 * 2048u >> 4);
+          const uint32_t pa = tS + 64u * half;
+#pragma unroll
+          for (int ks = 0; ks < 4; ++ks)
+            mma_ts(tO, pa + 8u * ks, vb + (uint32_t)ks * (2048u >> 4), kIdPV, !(due_first && half == 0 && ks == 0));
+          mma_commit(BAR(ODONE + 2 * tn + half));
+          if (half == 1) mma_commit(BAR(KVEMPTY + due_stage));
+        }
+        __syncwarp();
+        if (half == 1) {
+          ++units;
+          due = false;
+        }
+        return true;
+      };
+      for (int i = 0; ok; ++i) {
+        if (due && !(pv(0) && pv(1))) break;
+        if (!__all_sync(0xffffffffu, item_ready(i))) break;
+        const volatile Item& it = items[i % C::NIT];
+        const int n = __shfl_sync(0xffffffffu, it.n, 0), flags = __shfl_sync(0xffffffffu, it.flags, 0);
+        if (n == 0) break;
+        const bool one = flags & kSingle;
+        if (leader) mbar_arrive(BAR(ITEMPTY + i % C::NIT));
+        if (!wait(QFULL, (uint32_t)i)) break;
+        const uint32_t q_lo = desc_lo(sbase + C::OFF_Q, 16) + (one ? 0u : (uint32_t)tn * (C::TILE >> 4));
+        const int end = one ? n - ((n - 1 - tn) & 1) : n;   // one past this turn's last tile
+        if (end <= 0 && leader) mbar_arrive(BAR(QEMPTY));   // no unit for this turn
+        bool first = true;
+        for (int t = 0; t < n; ++t) {
+          if (due && !pv(0)) { ok = false; break; }
+          if (one) {
+            if (due && !pv(1)) { ok = false; break; }
+            if ((t & 1) != tn) {   // the other turn's tile: seen and passed over
+              for (int v = 0; v < 2 && ok; ++v) {
+                ok = wait(KVFULL + stage, phase);
+                if (leader) mbar_arrive(BAR(KVEMPTY + stage));
+                advance();
+              }
+              if (!ok) break;
+              continue;
+            }
+          }
+          if (!wait(KVFULL + stage, phase)) { ok = false; break; }
+          tc_fence_after();
+          const uint32_t kb = k_lo + stage * (C::TILE >> 4);
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            if (half == 1 && due && !pv(1)) { ok = false; break; }
+            if (leader) {
+#pragma unroll
+              for (int ks = 0; ks < D / 16; ++ks) {
+                const uint32_t off = ((uint32_t)(ks >> 2) * C::BLK + (uint32_t)(ks & 3) * 32u) >> 4;
+                mma_ss(tS + 64u * half, q_lo + off, kb + off + (uint32_t)half * (64u * 128u >> 4), kIdQK, ks != 0);
+              }
+              mma_commit(BAR(SFULL + 2 * tn + half));
+            }
+            __syncwarp();
+          }
+          if (!ok) break;
+          if (leader) {
+            mma_commit(BAR(KVEMPTY + stage));
+            if (t + 1 == end) mma_commit(BAR(QEMPTY));
           }
           __syncwarp();
-          ++sent;
+          advance();
+          due = true;
+          due_first = first;
+          due_stage = stage;
+          due_phase = phase;
+          advance();
+          first = false;
         }
-        if (!ok) break;
       }
-    }
-    if (*abort_flag && lane == 0) {   // let issued copies land
-      const uint32_t n = sent < (uint32_t)C::NST ? sent : (uint32_t)C::NST;
-      for (uint32_t k = sent - n; k < sent; ++k) mbar_wait_drain(BAR(KVFULL + k % C::NST), (k / C::NST) & 1u);
-    }
-  } else if (warp == C::WARP_Q) {
-    // ---------------- Q tiles
-    if (lane == 0) {
-      int merges = 0, sent = 0;
-      for (Units<BN> un(g, plan); un.w.live;) {
-        const bool one = un.single();
-        if (!mbar_wait(BAR(QEMPTY), (uint32_t)(un.items & 1) ^ 1u, abort_flag)) break;
-        // the second tile's place has been the buffer of the last merge
-        if (!one && merges > 0 && !mbar_wait(BAR(MERGED), (uint32_t)(merges - 1) & 1u, abort_flag)) break;
-        const uint32_t bytes = (uint32_t)(tpt * g.group) * 128u * C::NB;
-        mbar_arrive_expect_tx(BAR(QFULL), one ? bytes : 2 * bytes);
-        for (int s = 0; s < (one ? 1 : 2); ++s)
-#pragma unroll
-          for (int cb = 0; cb < C::NB; ++cb)
-            tma_load_3d(sbase + C::OFF_Q + s * C::TILE + cb * C::BLK, &tmQ, 64 * cb, un.w.h * g.group,
-                        un.w.s.q0 + un.w.i0 + s * tpt, BAR(QFULL));
-        ++sent;
-        merges += un.halves();
-        un.u = un.nu - 1;   // to the next item
-        un.next();
+      if (leader) {
+        mma_commit(BAR(DRAIN + tn));
+        mbar_wait_drain(BAR(DRAIN + tn), 0);
       }
-      if (*abort_flag && sent > 0) mbar_wait_drain(BAR(QFULL), (uint32_t)(sent - 1) & 1u);
+      __syncwarp();
     }
-  } else if (warp == C::WARP_MMA) {
-    // ---------------- MMA issuer
-    if (lane == 0) {
-      constexpr uint32_t kIdQK = idesc_bf16(128, BN, 0, 0);   // both K-major
-      constexpr uint32_t kIdPV = idesc_bf16(128, D, 0, 1);    // V: channels contiguous
-      Units<BN> qk(g, plan), pv(g, plan);
-      int nqk[2] = {0, 0}, npv[2] = {0, 0}, nitem[2] = {0, 0}, ahead = 0;
-      bool ok = true;
-      while (ok && pv.w.live) {
-        // scores run up to two units ahead, once the turn's P has been used
-        while (ok && qk.w.live && ahead < 2 && nqk[qk.turn()] == npv[qk.turn()]) {
-          const int tn = qk.turn();
-          if (qk.u == 0 && !mbar_wait(BAR(QFULL), (uint32_t)qk.items & 1u, abort_flag)) { ok = false; break; }
-          const uint32_t k = 2u * (uint32_t)(qk.base + qk.tile()), s = k % C::NST;
-          if (!mbar_wait(BAR(KVFULL + s), (k / C::NST) & 1u, abort_flag)) { ok = false; break; }
-          tc_fence_after();
-          const uint32_t qa = sbase + C::OFF_Q + (qk.single() ? 0u : (uint32_t)tn * C::TILE);
-          const uint32_t kb = sbase + C::OFF_KV + s * C::TILE;
-#pragma unroll
-          for (int ks = 0; ks < D / 16; ++ks) {
-            const uint32_t off = (uint32_t)(ks >> 2) * C::BLK + (uint32_t)(ks & 3) * 32u;
-            mma_bf16_ss(tmem + C::T_S + tn * 128u, desc_sw128(qa + off, 16, 1024), desc_sw128(kb + off, 16, 1024), kIdQK,
-                        ks != 0);
-          }
-          mma_commit(BAR(SFULL + tn));
-          if (qk.tile_ends()) mma_commit(BAR(KVEMPTY + s));
-          if (qk.u + 1 == qk.nu) mma_commit(BAR(QEMPTY));
-          ++nqk[tn];
-          ++ahead;
-          qk.next();
-        }
-        if (!ok) break;
-        const int tn = pv.turn();
-        const uint32_t k = 2u * (uint32_t)(pv.base + pv.tile()) + 1u, s = k % C::NST;
-        const bool first = pv.u < 2;   // of this turn in the item
-        if (!mbar_wait(BAR(KVFULL + s), (k / C::NST) & 1u, abort_flag)) break;
-        if (!mbar_wait(BAR(PFULL + tn), (uint32_t)npv[tn] & 1u, abort_flag)) break;
-        if (first) {   // the output of the last item has been read
-          if (!mbar_wait(BAR(OFREE + tn), (uint32_t)(nitem[tn] & 1) ^ 1u, abort_flag)) break;
-          ++nitem[tn];
-        }
-        tc_fence_after();
-        const uint32_t vb = sbase + C::OFF_KV + s * C::TILE;
-#pragma unroll
-        for (int ks = 0; ks < BN / 16; ++ks)
-          mma_bf16_ts(tmem + C::T_O + (uint32_t)tn * D, tmem + C::T_S + tn * 128u + 8u * ks,
-                      desc_sw128(vb + (uint32_t)ks * 2048u, C::BLK, 1024), kIdPV, !(first && ks == 0));
-        mma_commit(BAR(ODONE + tn));
-        if (pv.tile_ends()) mma_commit(BAR(KVEMPTY + s));
-        ++npv[tn];
-        --ahead;
-        pv.next();
-      }
-      mma_commit(BAR(DRAIN));
-      mbar_wait_drain(BAR(DRAIN), 0);
-    }
-    __syncwarp();
-  }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::REG_SOFTMAX));
     // ---------------- softmax and output: thread = row of its turn's tile
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::REG_SOFTMAX));
     const int tn = warp >> 2, r = tid & 127;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t tS = tmem + lanes + C::T_S + tn * 128u, tO = tmem + lanes + C::T_O + (uint32_t)tn * D;
     const int box = cv.page < BN ? cv.page : BN;
-    const int npg = BN / box;
-    const int ri = r / g.group, rg = r % g.group;   // token of the tile, head of the group
-    uint32_t cnt = 0;
-    int merges = 0;   // 64-row halves merged so far
+    const int ri = r / g.group;   // token of the tile
+    uint32_t cnt = 0;             // units of this turn so far
+    uint32_t base = 0;            // key tiles before the item
+    int merges = 0;               // 64-row halves merged so far
+    auto arrive = [&](int bar) {   // the warp's one arrival, after its lanes' TMEM and shared-memory accesses
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(BAR(bar));
+    };
+    auto wait = [&](int bar, uint32_t phase) -> bool {
+      return warp_wait(BAR(bar), phase & 1u, abort_flag);
+    };
+    // The turns' exponentials alternate: left alone, the two warps of an SM
+    // quarter end up in step, share the XU pipe and then leave it idle together
+    // (4500 cycles for 128 keys of both turns).  Round k of turn 0 follows
+    // round k - 1 of turn 1, round k of turn 1 follows round k of turn 0.
+    uint32_t rounds = 0;
+    auto exp_begin = [&]() -> bool {
+      if (tn == 0 && rounds == 0) return true;
+      return wait(EXPED + (tn ^ 1) * 4 + (warp & 3), tn ? rounds : rounds - 1u);
+    };
+    auto exp_end = [&]() {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(BAR(EXPED + tn * 4 + (warp & 3)));
+      ++rounds;
+    };
     bool ok = true;
-    Meta meta{0, 0, 0, 0};
-    for (Units<BN> un(g, plan); ok && un.w.live;) {
-      const Walk<BN>& w = un.w;
-      const bool one = un.single();
+    for (int i = 0; ok; ++i) {
+      if (!__all_sync(0xffffffffu, item_ready(i))) break;
+      const volatile Item& it = items[i % C::NIT];
+      const int n = it.n;
+      if (n == 0) break;
+      const int flags = it.flags;
+      const bool one = flags & kSingle;
       const int tok = (one ? 0 : tn * tpt) + ri;      // of the item
-      const bool valid = ri < tpt && tok < w.ntok;
+      const bool valid = ri < tpt && tok < it.ntok;
       const bool busy = __any_sync(0xffffffffu, valid);
       Span sp{0, 0, 0};
-      if (valid) sp = span_of(g, w.s.len - w.s.n + w.i0 + tok, w.s.len);
+      if (valid) sp = span_of(g, it.pos0 + tok, it.len);
       float m = neg_inf(), l = 0.f;
-      const int n = w.n();
       int done = 0;   // units of this turn
-      for (int t = one ? tn : 0; t < n; t += one ? 2 : 1, ++cnt, ++done) {
-        const int j0 = key_tile(w.tiles, w.t0 + t) * BN;
-        // pages of the tile that do not exist
-        bool gone = false;
-        if (lane < npg && j0 + lane * box < w.s.len) {
-          const int id = __ldg(cv.table + (int64_t)w.b * cv.table_stride + (j0 + lane * box) / cv.page);
-          gone = id < 0 || id >= cv.pages;
-        }
-        if (!__all_sync(0xffffffffu, mbar_wait(BAR(SFULL + tn), cnt & 1u, abort_flag))) { ok = false; break; }
-        tc_fence_after();
-        const unsigned absent = __ballot_sync(0xffffffffu, gone);
-        // keys of the tile that no row of the item sees: their values may be
-        // anything (0 x NaN would reach the sums), so they become zeros
-        const bool inside = j0 + BN <= w.tiles.anc || (j0 >= w.tiles.lo && j0 + BN <= w.tiles.end);
-        if (!inside) {
-          const uint32_t k = 2u * (uint32_t)(un.base + t) + 1u, s = k % C::NST;
-          if (!__all_sync(0xffffffffu, mbar_wait(BAR(KVFULL + s), (k / C::NST) & 1u, abort_flag))) { ok = false; break; }
-          const int j = j0 + r;
-          if (!(j < w.tiles.anc || (j >= w.tiles.lo && j < w.tiles.end))) {
-            const uint32_t at = sbase + C::OFF_KV + s * C::TILE + (uint32_t)r * 128u;
+      for (int t = one ? tn : 0; ok && t < n; t += one ? 2 : 1, ++cnt, ++done) {
+        const int kt = it.t0 + t, na = it.n_anchor;
+        const int j0 = (kt < na ? kt : it.first + (kt - na)) * BN;
+        uint32_t absent = 0u;   // pages of the tile that do not exist
+        bool masked = false;    // some row of the warp does not see the whole tile
 #pragma unroll
-            for (int cb = 0; cb < C::NB; ++cb)
+        for (int half = 0; half < 2; ++half) {
+          if (!wait(SFULL + 2 * tn + half, cnt)) { ok = false; break; }
+          tc_fence_after();
+          // keys of the tile that no row of the item sees: their values may be
+          // anything (0 x NaN would reach the sums), so they become zeros
+          if (half == 0 && !(j0 + BN <= it.anc || (j0 >= it.lo && j0 + BN <= it.end))) {
+            const uint32_t k = 2u * (base + (uint32_t)t) + 1u, s = k % C::NST;
+            if (!wait(KVFULL + s, k / C::NST)) { ok = false; break; }
+            const int j = j0 + r;
+            if (!(j < it.anc || (j >= it.lo && j < it.end))) {
+              const uint32_t at = sbase + C::OFF_KV + s * C::TILE + (uint32_t)r * 128u;
 #pragma unroll
-              for (int c = 0; c < 8; ++c) st_shared_v4(at + cb * C::BLK + 16u * c, make_uint4(0u, 0u, 0u, 0u));
+              for (int cb = 0; cb < C::NB; ++cb)
+#pragma unroll
+                for (int c = 0; c < 8; ++c) st_shared_v4(at + cb * C::BLK + 16u * c, make_uint4(0u, 0u, 0u, 0u));
+            }
+            fence_proxy_async_smem();
           }
-          fence_proxy_async_smem();
-        }
-        if (busy) {
-          uint32_t v[4][32];
-#pragma unroll
-          for (int c = 0; c < 4; ++c) tmem_ld32(tS + 32u * c, v[c]);
+          if (!busy) {
+            if (!exp_begin()) { ok = false; break; }
+            exp_end();
+            arrive(PFULL + 2 * tn + half);
+            continue;
+          }
+          const uint32_t tSh = tS + 64u * half;
+          const int jh = j0 + 64 * half;
+          uint32_t v[2][32];
+          tmem_ld32(tSh, v[0]);
+          tmem_ld32(tSh + 32u, v[1]);
+          if (half == 0) {
+            absent = gone[(base + (uint32_t)t) % C::NGONE];
+            const bool all = !valid || j0 + BN <= sp.anc || (j0 >= sp.lo && j0 + BN <= sp.end);
+            masked = !__all_sync(0xffffffffu, all && absent == 0u);
+          }
           tmem_wait_ld();
-          const bool all = !valid || j0 + BN <= sp.anc || (j0 >= sp.lo && j0 + BN <= sp.end);
-          if (absent || !__all_sync(0xffffffffu, all)) {
+          if (masked) {
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              const uint32_t see = seen_word(sp, j0 + 32 * c) & ~absent_word(absent, c, box);
+            for (int c = 0; c < 2; ++c) {
+              const uint32_t see = seen_word(sp, jh + 32 * c) & ~absent_word(absent, 2 * half + c, box);
 #pragma unroll
-              for (int i = 0; i < 32; ++i)
-                if (!((see >> i) & 1u)) v[c][i] = 0xff800000u;
+              for (int e = 0; e < 32; ++e)
+                if (!((see >> e) & 1u)) v[c][e] = 0xff800000u;
             }
           }
           float mx[4];
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
-            mx[c] = __uint_as_float(v[c][0]);
+            const uint32_t* x = v[c >> 1] + 16 * (c & 1);
+            mx[c] = __uint_as_float(x[0]);
 #pragma unroll
-            for (int i = 1; i < 32; ++i) mx[c] = fmaxf(mx[c], __uint_as_float(v[c][i]));
+            for (int e = 1; e < 15; e += 2) mx[c] = fmaxf(fmaxf(mx[c], __uint_as_float(x[e])), __uint_as_float(x[e + 1]));
+            mx[c] = fmaxf(mx[c], __uint_as_float(x[15]));
           }
           const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
           // a row's first keys set its maximum; later it moves when outgrown
@@ -364,63 +576,61 @@ k_attn_tc(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUten
           if (__any_sync(0xffffffffu, grow)) {
             const float alpha = grow ? ex2((m - top) * c2) : 1.f;
             l *= alpha;
-            if (!__all_sync(0xffffffffu, mbar_wait(BAR(ODONE + tn), (cnt - 1u) & 1u, abort_flag))) { ok = false; break; }
+            if (!wait(ODONE + 2 * tn + (half ^ 1), half ? cnt : cnt - 1u)) { ok = false; break; }
             tc_fence_after();
 #pragma unroll 1
-            for (int c = 0; c < D / 32; ++c) {
-              uint32_t o[32];
-              tmem_ld32(tO + 32u * c, o);
+            for (int c = 0; c < D / 16; ++c) {
+              uint32_t o[16];
+              tmem_ld16(tO + 16u * c, o);
               tmem_wait_ld();
 #pragma unroll
-              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
-              tmem_st32(tO + 32u * c, o);
+              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+              tmem_st16(tO + 16u * c, o);
             }
           }
           if (grow || m == neg_inf()) m = top;
-          const float base = m == neg_inf() ? 0.f : m * c2;
+          const float nb = m == neg_inf() ? 0.f : -m * c2;
+          if (!exp_begin()) { ok = false; break; }
           float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            uint32_t p[32];
+          for (int c = 0; c < 2; ++c) {
+            uint32_t p[16];
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              const int e = 64 * h + 2 * i;
-              const float a = ex2(fmaf(__uint_as_float(v[e >> 5][e & 31]), c2, -base));
-              const float b = ex2(fmaf(__uint_as_float(v[(e + 1) >> 5][(e + 1) & 31]), c2, -base));
-              sum[2 * (i & 1)] += a;
-              sum[2 * (i & 1) + 1] += b;
-              p[i] = pack_bf16(a, b);
+            for (int e = 0; e < 16; ++e) {
+              // scalar, not paired, arithmetic: with one warp of an SM quarter at
+              // work 64 keys take 592 cycles instead of 765 (512 of the XU pipe)
+              const float a = ex2(fmaf(__uint_as_float(v[c][2 * e]), c2, nb));
+              const float b = ex2(fmaf(__uint_as_float(v[c][2 * e + 1]), c2, nb));
+              sum[2 * (e & 1)] += a;
+              sum[2 * (e & 1) + 1] += b;
+              p[e] = pack_bf16(a, b);
             }
-            tmem_st32(tS + 32u * h, p);
+            tmem_st16(tSh + 16u * c, p);
           }
+          exp_end();
           l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
           tmem_wait_st();
+          arrive(PFULL + 2 * tn + half);
         }
-        tc_fence_before();
-        mbar_arrive(BAR(PFULL + tn));
       }
+      if (one && tn == 1 && (n & 1))   // turn 0 has one unit more
+        for (int half = 0; ok && half < 2; ++half) {
+          ok = exp_begin();
+          exp_end();
+        }
       if (!ok) break;
+      base += (uint32_t)n;
       if (done > 0) {   // the turn's last product
-        if (!__all_sync(0xffffffffu, mbar_wait(BAR(ODONE + tn), (cnt - 1u) & 1u, abort_flag))) break;
+        if (!wait(ODONE + 2 * tn + 1, cnt - 1u)) break;
         tc_fence_after();
-      }
-      const bool whole = w.whole();
-      const int slot = w.t0 > 0 ? 0 : 1;
-      const int tok0 = w.s.q0 + w.i0;
-      if (!whole && slot == 1) {   // begun here, continued in later shares
-        const long long start = plan.w1 - n;
-        meta.parts = share_of(plan.W, start + w.tiles.count - 1, plan.shares) - (int)blockIdx.x + 1;
-        meta.tok0 = tok0;
-        meta.h = w.h;
-        meta.rows = w.ntok * g.group;
       }
       // rows of a single tile: turn 1 hands its sums to turn 0 in shared
       // memory, 64 rows at a time
-      const int halves = un.halves();
+      const int halves = flags >> kHalfShift;
       const uint32_t xr = (uint32_t)(r & 63) * 16u, xb = sbase + C::OFF_Q + C::TILE, xml = sbase + C::OFF_ML + 8u * (uint32_t)(r & 63);
       if (one && tn == 1) {
         for (int half = 0; half < halves; ++half, ++merges) {
-          if (merges > 0 && !__all_sync(0xffffffffu, mbar_wait(BAR(MERGED), (uint32_t)(merges - 1) & 1u, abort_flag))) { ok = false; break; }
+          if (merges > 0 && !wait(MERGED, (uint32_t)(merges - 1))) { ok = false; break; }
           if ((r >> 6) == half && busy) {
 #pragma unroll 1
             for (int c = 0; c < D / 32; ++c) {
@@ -428,23 +638,24 @@ k_attn_tc(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUten
               tmem_ld32(tO + 32u * c, o);
               tmem_wait_ld();
 #pragma unroll
-              for (int i = 0; i < 8; ++i)
-                st_shared_v4(xb + (uint32_t)(8 * c + i) * 1024u + xr, make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]));
+              for (int e = 0; e < 8; ++e)
+                st_shared_v4(xb + (uint32_t)(8 * c + e) * 1024u + xr, make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]));
             }
             st_shared_f1(xml, m);
             st_shared_f1(xml + 4u, l);
           }
           fence_proxy_async_smem();
-          mbar_arrive(BAR(HANDED));
+          arrive(HANDED);
         }
       } else {
-        const int tokg = tok0 + tok, hd = w.h * g.group + rg;
-        const size_t prow = ((size_t)blockIdx.x * 2 + slot) * parts.rows + (one ? 0 : tn * tpt * g.group) + r;
+        const bool whole = flags & kWhole;
+        const int tokg = it.tok0 + tok, hd = it.h * g.group + r % g.group;
+        const size_t prow = ((size_t)blockIdx.x * 2 + (flags & kLast ? 1 : 0)) * parts.rows + (one ? 0 : tn * tpt * g.group) + r;
         const int passes = halves > 0 ? halves : 1;
         for (int half = 0; half < passes; ++half) {
           float ms = m, lt = l, f0 = 1.f, f1 = 0.f;   // maximum and sum of both turns; scales of this turn's and the other's output
           if (halves > 0) {
-            if (!__all_sync(0xffffffffu, mbar_wait(BAR(HANDED), (uint32_t)merges & 1u, abort_flag))) { ok = false; break; }
+            if (!wait(HANDED, (uint32_t)merges)) { ok = false; break; }
             ++merges;
             const float m1 = ld_shared_f1(xml), l1 = ld_shared_f1(xml + 4u);
             ms = fmaxf(m, m1);
@@ -465,32 +676,32 @@ k_attn_tc(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUten
               tmem_wait_ld();
               float x[32];
 #pragma unroll
-              for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(o[i]) * f0;
+              for (int e = 0; e < 32; ++e) x[e] = __uint_as_float(o[e]) * f0;
               if (halves > 0) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                  const float4 y = ld_shared_f4(xb + (uint32_t)(8 * c + i) * 1024u + xr);
-                  x[4 * i] = fmaf(y.x, f1, x[4 * i]);
-                  x[4 * i + 1] = fmaf(y.y, f1, x[4 * i + 1]);
-                  x[4 * i + 2] = fmaf(y.z, f1, x[4 * i + 2]);
-                  x[4 * i + 3] = fmaf(y.w, f1, x[4 * i + 3]);
+                for (int e = 0; e < 8; ++e) {
+                  const float4 y = ld_shared_f4(xb + (uint32_t)(8 * c + e) * 1024u + xr);
+                  x[4 * e] = fmaf(y.x, f1, x[4 * e]);
+                  x[4 * e + 1] = fmaf(y.y, f1, x[4 * e + 1]);
+                  x[4 * e + 2] = fmaf(y.z, f1, x[4 * e + 2]);
+                  x[4 * e + 3] = fmaf(y.w, f1, x[4 * e + 3]);
                 }
               }
               if (none) {
 #pragma unroll
-                for (int i = 0; i < 32; ++i) x[i] = 0.f;
+                for (int e = 0; e < 32; ++e) x[e] = 0.f;
               }
               if (valid) {
                 if (whole) {
                   uint4* dst = reinterpret_cast<uint4*>(ov.out + (int64_t)tokg * ov.ts + (int64_t)hd * ov.hs + 32 * c);
 #pragma unroll
-                  for (int i = 0; i < 4; ++i)
-                    dst[i] = make_uint4(pack_bf16(x[8 * i], x[8 * i + 1]), pack_bf16(x[8 * i + 2], x[8 * i + 3]),
-                                        pack_bf16(x[8 * i + 4], x[8 * i + 5]), pack_bf16(x[8 * i + 6], x[8 * i + 7]));
+                  for (int e = 0; e < 4; ++e)
+                    dst[e] = make_uint4(pack_bf16(x[8 * e], x[8 * e + 1]), pack_bf16(x[8 * e + 2], x[8 * e + 3]),
+                                        pack_bf16(x[8 * e + 4], x[8 * e + 5]), pack_bf16(x[8 * e + 6], x[8 * e + 7]));
                 } else {
                   float4* dst = reinterpret_cast<float4*>(parts.o + prow * D + 32 * c);
 #pragma unroll
-                  for (int i = 0; i < 8; ++i) dst[i] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+                  for (int e = 0; e < 8; ++e) dst[e] = make_float4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
                 }
               }
             }
@@ -502,17 +713,16 @@ k_attn_tc(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUten
           }
           if (halves > 0) {   // the buffer is free for the next rows, or the next Q tile
             fence_proxy_async_smem();
-            mbar_arrive(BAR(MERGED));
+            arrive(MERGED);
+            if (lane == 0) count_add(merged);
           }
         }
       }
       if (!ok) break;
-      tc_fence_before();
-      if (done > 0) mbar_arrive(BAR(OFREE + tn));
-      un.u = un.nu - 1;   // to the next item
-      un.next();
+      if (done > 0) arrive(OFREE + tn);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(BAR(ITEMPTY + i % C::NIT));
     }
-    if (tid == 0) parts.meta[blockIdx.x] = meta;
   }
 
   tc_fence_before();

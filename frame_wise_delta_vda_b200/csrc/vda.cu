@@ -538,6 +538,9 @@ int vda_paged_attention(const vda_attn_args* a, void* workspace, size_t workspac
   if (!rows_ok(a->q, a->N, a->Hq, es) || !rows_out_ok(a->out, a->N, a->Hq, a->d, es)) return VDA_ERR_INVALID_ARGUMENT;
   const vda::attn::AttnPlan p =
       vda::attn::make_attn_plan(a->dtype, a->Hq, a->Hk, a->d, a->page_size, a->N, a->B, vda::tc::num_sms());
+  // every CTA's share is counted in 32 bits
+  const double items = ((double)a->N / p.tpi + a->B) * a->Hk, keys = (double)a->max_pages * a->page_size;
+  if (items * (keys / 64 + 2) > 2147483647.0) return VDA_ERR_UNSUPPORTED;
   // the tensor map of q steps over at least 16 and less than 2^40 bytes
   if (p.tc && ((a->N > 1 && (a->q.token_stride < 8 || a->q.token_stride >= (1LL << 39))) ||
                (a->Hq > 1 && (a->q.head_stride < 8 || a->q.head_stride >= (1LL << 39)))))
@@ -578,7 +581,7 @@ int vda_qk_norm_rope(const vda_qk_args* a) {
 
 size_t vda_qk_grad_workspace_bytes(int d) {
   if (d != 16 && d != 32 && d != 64 && d != 128) return 0;
-  return (size_t)vda::qk::kBwdMaxBlocks * 2 * d * sizeof(float);
+  return (size_t)vda::qk::kBwdMaxBlocks * d * sizeof(float);
 }
 
 int vda_qk_norm_rope_backward(const vda_qk_grad_args* a, void* workspace, size_t workspace_bytes) {
