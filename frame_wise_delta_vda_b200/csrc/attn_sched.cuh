@@ -118,23 +118,17 @@ __device__ __forceinline__ Seq load_seq(const Geom& g, int b) {
   return make_seq(g, __ldg(g.q_start + b), __ldg(g.q_start + b + 1), __ldg(g.kv_len + b));
 }
 
-// Tiles of one head of a sequence, computed by one lane.
+// What follows runs once a CTA, on code that no cache holds yet: a fetch of
+// instructions costs as much as a load of data, so it is kept small (one copy of
+// the counting, called) rather than unrolled.
 template <int BN>
-__device__ __forceinline__ int seq_tiles_serial(const Geom& g, const Seq& s) {
-  int w = 0;
-  const int n = items_of(g, s.n);
-  for (int r = 0; r < n; ++r) w += tiles_of<BN>(g, s, r * g.tpi, imin(g.tpi, s.n - r * g.tpi)).count;
-  return w;
-}
-// ... and by a whole warp.
-template <int BN>
-__device__ __forceinline__ int seq_tiles_warp(const Geom& g, const Seq& s, int lane) {
-  int w = 0;
-  const int n = items_of(g, s.n);
-  for (int r = lane; r < n; r += 32) w += tiles_of<BN>(g, s, r * g.tpi, imin(g.tpi, s.n - r * g.tpi)).count;
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) w += __shfl_xor_sync(0xffffffffu, w, off);
-  return w;
+__device__ __noinline__ int item_tiles(const Geom& g, int n, int len, int r) {
+  Seq s;
+  s.q0 = 0;
+  s.n = n;
+  s.len = len;
+  const int i0 = r * g.tpi;
+  return tiles_of<BN>(g, s, i0, imin(g.tpi, n - i0)).count;
 }
 
 // Where a CTA's share begins.
@@ -149,48 +143,55 @@ constexpr int kSerialItems = 4;   // longer sequences are counted by the whole w
 
 // One head's tiles of sequences 32 c .. 32 c + 31, one a lane.
 template <int BN>
-__device__ __forceinline__ int chunk_tiles(const Geom& g, int c, int lane) {
+__device__ __noinline__ int chunk_tiles(const Geom& g, int c, int lane) {
   const int b = c * 32 + lane;
   Seq s{0, 0, 0};
   if (b < g.B) s = load_seq(g, b);
+  const int n = items_of(g, s.n);
+  const bool longer = n > kSerialItems;
   int w = 0;
-  const bool longer = items_of(g, s.n) > kSerialItems;
-  if (!longer) w = seq_tiles_serial<BN>(g, s);
+#pragma unroll 1
+  for (int r = 0; r < n && !longer; ++r) w += item_tiles<BN>(g, s.n, s.len, r);
+  __syncwarp();
   unsigned todo = __ballot_sync(0xffffffffu, longer);
+#pragma unroll 1
   while (todo) {
     const int l = __ffs(todo) - 1;
     todo &= todo - 1;
-    Seq o;
-    o.q0 = 0;
-    o.n = __shfl_sync(0xffffffffu, s.n, l);
-    o.len = __shfl_sync(0xffffffffu, s.len, l);
-    const int v = seq_tiles_warp<BN>(g, o, lane);
+    const int sn = __shfl_sync(0xffffffffu, s.n, l), sl = __shfl_sync(0xffffffffu, s.len, l);
+    int v = 0;
+#pragma unroll 1
+    for (int r = lane; r < items_of(g, sn); r += 32) v += item_tiles<BN>(g, sn, sl, r);
+    v = __reduce_add_sync(0xffffffffu, v);
     if (lane == l) w = v;
   }
   return w;
 }
 
-// One warp finds share `cta` of `ctas`.  The first kKeep chunks of 32
-// sequences are counted once and kept in registers.  The host bounds W for
-// ascending q_start; sequences that overlap so that W passes 2^31 get nothing.
+__device__ __noinline__ int prefix_sum(int v, int lane) {   // inclusive, over the warp
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int u = __shfl_up_sync(0xffffffffu, v, off);
+    if (lane >= off) v += u;
+  }
+  return v;
+}
+
+// One warp finds share `cta` of `ctas`.  The host bounds W below 2^31 for
+// ascending q_start; overlapping sequences may pass it and get wrong results,
+// within the tensors all the same.
 template <int BN>
 __device__ __forceinline__ Plan plan_share(const Geom& g, int cta, int ctas, int lane) {
-  constexpr int kKeep = 4;
-  int keep[kKeep];
-  long long total = 0;
   const int chunks = (g.B + 31) / 32;
-#pragma unroll
-  for (int c = 0; c < kKeep; ++c) {
-    keep[c] = c < chunks ? chunk_tiles<BN>(g, c, lane) : 0;
-    total += keep[c];
-  }
+  int total = 0, kept = 0;   // kept: the first chunk's tiles, all there are up to 32 sequences
 #pragma unroll 1
-  for (int c = kKeep; c < chunks; ++c) total += chunk_tiles<BN>(g, c, lane);
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) total += __shfl_xor_sync(0xffffffffu, total, off);
-  total *= g.Hk;
+  for (int c = 0; c < chunks; ++c) {
+    const int w = chunk_tiles<BN>(g, c, lane);
+    if (c == 0) kept = w;
+    total += w;
+  }
   Plan p;
-  p.W = total > 2147483647LL ? 0 : (int)total;
+  p.W = imax(0, __reduce_add_sync(0xffffffffu, total) * g.Hk);
   p.w0 = p.w1 = p.b = p.h = p.r = p.t = 0;
   p.shares = imin(p.W, ctas);
   if (cta >= p.shares) return p;
@@ -199,20 +200,8 @@ __device__ __forceinline__ Plan plan_share(const Geom& g, int cta, int ctas, int
   int rest = p.w0;   // tiles still to pass
 #pragma unroll 1
   for (int c = 0; c < chunks; ++c) {
-    int w = 0;
-    if (c < kKeep) {
-#pragma unroll
-      for (int k = 0; k < kKeep; ++k)
-        if (c == k) w = keep[k];
-    } else {
-      w = chunk_tiles<BN>(g, c, lane);
-    }
-    int upto = w * g.Hk;   // inclusive prefix over the lanes
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const int v = __shfl_up_sync(0xffffffffu, upto, off);
-      if (lane >= off) upto += v;
-    }
+    const int w = c == 0 ? kept : chunk_tiles<BN>(g, c, lane);
+    const int upto = prefix_sum(w * g.Hk, lane);
     const unsigned hit = __ballot_sync(0xffffffffu, upto > rest);
     if (!hit) {
       rest -= __shfl_sync(0xffffffffu, upto, 31);
@@ -227,16 +216,16 @@ __device__ __forceinline__ Plan plan_share(const Geom& g, int cta, int ctas, int
     // the run of tokens that holds tile `rest` of this head
     const Seq s = load_seq(g, p.b);
     const int n = items_of(g, s.n);
+    if (n == 1) {
+      p.t = rest;
+      break;
+    }
 #pragma unroll 1
     for (int r0 = 0; r0 < n; r0 += 32) {
       const int r = r0 + lane;
-      const int k = r < n ? tiles_of<BN>(g, s, r * g.tpi, imin(g.tpi, s.n - r * g.tpi)).count : 0;
-      int pre = k;
-#pragma unroll
-      for (int off = 1; off < 32; off <<= 1) {
-        const int v = __shfl_up_sync(0xffffffffu, pre, off);
-        if (lane >= off) pre += v;
-      }
+      const int k = r < n ? item_tiles<BN>(g, s.n, s.len, r) : 0;
+      __syncwarp();
+      const int pre = prefix_sum(k, lane);
       const unsigned at = __ballot_sync(0xffffffffu, pre > rest);
       if (at) {
         const int rl = __ffs(at) - 1;

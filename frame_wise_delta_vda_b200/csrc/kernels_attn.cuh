@@ -333,12 +333,11 @@ struct AttnPlan {
   size_t off_ml, off_meta, total;
 };
 
-// The tensor-core kernel takes bf16 of d = 64 and 128 in pages that tile 128
-// keys in whole 8-row groups (or are tiled by 128 keys), up to 128 query heads
-// a KV head; the SIMT kernel everything else, up to 64.
+// The tensor-core kernel takes bf16 of d = 64 and 128 in pages of a power of two
+// from 8 tokens (a box of a TMA load: whole groups of 8 rows of the swizzle), up
+// to 128 query heads a KV head; the SIMT kernel everything else, up to 64.
 inline bool tc_supported(int dtype, int d, int group, int page) {
-  const bool pages = page >= 128 ? page % 128 == 0 : page >= 8 && 128 % page == 0;
-  return dtype == VDA_BF16 && (d == 64 || d == 128) && group <= 128 && pages;
+  return dtype == VDA_BF16 && (d == 64 || d == 128) && group <= 128 && page >= 8 && (page & (page - 1)) == 0;
 }
 
 inline AttnPlan make_attn_plan(int dtype, int Hq, int Hk, int d, int page, long long N, int B, int sms) {

@@ -125,15 +125,14 @@ struct TcCfg {
   static constexpr uint32_t OFF_ITEM = OFF_ML + 64 * 8;
   static constexpr uint32_t OFF_GONE = OFF_ITEM + NIT * 64;
   static constexpr uint32_t OFF_BAR = OFF_GONE + NGONE * 4;
-  // kvfull[NST], kvempty[NST], itfull[NIT], itempty[NIT], qfull, qempty, sfull[2][2], pfull[2][2], odone[2][2], ofree[2],
+  // kvfull[NST], kvempty[NST], itfull[NIT], itempty[NIT], qfull, qempty, sfull[2], pfull[2][2], odone[2], ofree[2],
   // handed, merged, drain[2], exped[2][4]
-  static constexpr int NBAR = 2 * NST + 2 * NIT + 28;
+  static constexpr int NBAR = 2 * NST + 2 * NIT + 24;
   static constexpr size_t SMEM = OFF_BAR + NBAR * 8 + 16 + 1024;   // + TMEM address, abort flag, merge count
   static constexpr int WARP_KV = 8, WARP_MMA = 9, WARP_ITEM = 11, THREADS = 384;
   // registers: 384 threads x 168 at launch = 64512 >= 256 x 200 + 128 x 96 after the split
   static constexpr int REG_SOFTMAX = 200, REG_OTHER = 96;
-  // TMEM columns: S of turn 0, 1, each in halves of 64 keys (a half's P over its
-  // first 32 columns); output of turn 0, 1
+  // TMEM columns: S (P over its first half) of turn 0, 1; output of turn 0, 1
   static constexpr uint32_t T_S = 0, T_O = 256, T_COLS = 512;
 };
 
@@ -167,7 +166,7 @@ k_attn_tc(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUten
   const uint32_t sbase = smem_u32(smem);
   auto BAR = [&](int i) -> uint32_t { return sbase + C::OFF_BAR + 8u * (uint32_t)i; };
   constexpr int KVFULL = 0, KVEMPTY = C::NST, ITFULL = 2 * C::NST, ITEMPTY = ITFULL + C::NIT, QFULL = ITEMPTY + C::NIT,
-                QEMPTY = QFULL + 1, SFULL = QFULL + 2, PFULL = SFULL + 4, ODONE = PFULL + 4, OFREE = ODONE + 4,
+                QEMPTY = QFULL + 1, SFULL = QFULL + 2, PFULL = SFULL + 2, ODONE = PFULL + 4, OFREE = ODONE + 2,
                 HANDED = OFREE + 2, MERGED = HANDED + 1, DRAIN = MERGED + 1,
                 EXPED = DRAIN + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_BAR + C::NBAR * 8);
@@ -189,12 +188,9 @@ k_attn_tc(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUten
     mbar_init(BAR(QFULL), 1);
     mbar_init(BAR(QEMPTY), 2);
     for (int s = 0; s < 2; ++s) {
-      mbar_init(BAR(SFULL + 2 * s), 1);
-      mbar_init(BAR(SFULL + 2 * s + 1), 1);
-      mbar_init(BAR(PFULL + 2 * s), 4);
-      mbar_init(BAR(PFULL + 2 * s + 1), 4);
-      mbar_init(BAR(ODONE + 2 * s), 1);
-      mbar_init(BAR(ODONE + 2 * s + 1), 1);
+      mbar_init(BAR(SFULL + s), 1);
+      for (int p = 0; p < 2; ++p) mbar_init(BAR(PFULL + 2 * s + p), 4);
+      mbar_init(BAR(ODONE + s), 1);
       mbar_init(BAR(OFREE + s), 4);
     }
     mbar_init(BAR(HANDED), 4);
@@ -205,6 +201,10 @@ k_attn_tc(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUten
     *abort_flag = 0;
     *merged = 0u;
     fence_mbar_init();
+  }
+  if (tid == 32) {
+    for (const CUtensorMap* m : {&tmQ, &tmK, &tmV})
+      asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(m)) : "memory");
   }
   if (warp == C::WARP_MMA) {
     tmem_alloc(smem_u32(tmem_slot), C::T_COLS);
@@ -234,51 +234,56 @@ k_attn_tc(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUten
       if (lane == 0) {
         Meta meta{0, 0, 0, 0};
         Walk<BN> w(g, plan);
-        auto publish = [&](int i) -> bool {
-          const int s = i % C::NIT;
-          if (!mbar_wait(BAR(ITEMPTY + s), ((uint32_t)(i / C::NIT) & 1u) ^ 1u, abort_flag)) return false;
-          volatile Item& it = items[s];
-          it.n = w.live ? w.n() : 0;
-          if (w.live) {
-            const bool single = 2 * w.ntok <= g.tpi, last = !w.whole() && w.t0 == 0;
-            const int rows = w.ntok * g.group;
-            it.b = w.b;
-            it.h = w.h;
-            it.tok0 = w.s.q0 + w.i0;
-            it.ntok = w.ntok;
-            it.pos0 = w.s.len - w.s.n + w.i0;
-            it.len = w.s.len;
-            it.lo = w.tiles.lo;
-            it.end = w.tiles.end;
-            it.anc = w.tiles.anc;
-            it.n_anchor = w.tiles.n_anchor;
-            it.first = w.tiles.first;
-            it.t0 = w.t0;
-            it.flags = (single ? kSingle : 0) | (w.whole() ? kWhole : 0) | (last ? kLast : 0) |
-                       ((single && w.n() > 1 ? (rows > 64 ? 2 : 1) : 0) << kHalfShift);
-            if (last) {
-              meta.parts = share_of(plan.W, plan.w1 - w.n() + w.tiles.count - 1, plan.shares) - (int)blockIdx.x + 1;
-              meta.tok0 = w.s.q0 + w.i0;
-              meta.h = w.h;
-              meta.rows = rows;
+        int merges = 0, sent = 0, listed = 0;
+        bool more = true;   // items to list
+        while (true) {
+          // one item is listed ahead of the Q tile that is sent, for K and V to
+          // follow without a gap; the first Q tile goes at once
+          if (more && (listed == 0 || (sent > 0 && listed <= sent + 1))) {
+            const int s = listed % C::NIT;
+            if (!mbar_wait(BAR(ITEMPTY + s), ((uint32_t)(listed / C::NIT) & 1u) ^ 1u, abort_flag)) break;
+            volatile Item& it = items[s];
+            it.n = w.live ? w.n() : 0;
+            if (w.live) {
+              const bool single = 2 * w.ntok <= g.tpi, last = !w.whole() && w.t0 == 0;
+              const int rows = w.ntok * g.group;
+              it.b = w.b;
+              it.h = w.h;
+              it.tok0 = w.s.q0 + w.i0;
+              it.ntok = w.ntok;
+              it.pos0 = w.s.len - w.s.n + w.i0;
+              it.len = w.s.len;
+              it.lo = w.tiles.lo;
+              it.end = w.tiles.end;
+              it.anc = w.tiles.anc;
+              it.n_anchor = w.tiles.n_anchor;
+              it.first = w.tiles.first;
+              it.t0 = w.t0;
+              it.flags = (single ? kSingle : 0) | (w.whole() ? kWhole : 0) | (last ? kLast : 0) |
+                         ((single && w.n() > 1 ? (rows > 64 ? 2 : 1) : 0) << kHalfShift);
+              if (last) {
+                meta.parts = share_of(plan.W, plan.w1 - w.n() + w.tiles.count - 1, plan.shares) - (int)blockIdx.x + 1;
+                meta.tok0 = w.s.q0 + w.i0;
+                meta.h = w.h;
+                meta.rows = rows;
+              }
             }
+            mbar_arrive(BAR(ITFULL + s));
+            ++listed;
+            more = w.live;
+            if (more) w.next();
+            continue;
           }
-          mbar_arrive(BAR(ITFULL + s));
-          if (w.live) w.next();
-          return true;
-        };
-        int merges = 0, sent = 0;
-        bool ok = publish(0);
-        for (int i = 0; ok && items[i % C::NIT].n != 0; ++i) {
-          const volatile Item& it = items[i % C::NIT];   // its place is not used again before item i + NIT
-          if (!publish(i + 1)) break;
+          const volatile Item& it = items[sent % C::NIT];   // its place is not used again before item sent + NIT
+          if (it.n == 0) break;
           const int flags = it.flags, h = it.h, tok0 = it.tok0;
           const bool one = flags & kSingle;
-          if (!mbar_wait(BAR(QEMPTY), (uint32_t)(i & 1) ^ 1u, abort_flag)) break;
+          if (!mbar_wait(BAR(QEMPTY), (uint32_t)(sent & 1) ^ 1u, abort_flag)) break;
           // the second tile's place has been the buffer of the last merge
           if (!one && !count_wait(merged, 4u * (uint32_t)merges, abort_flag)) break;
           const uint32_t bytes = (uint32_t)(tpt * g.group) * 128u * C::NB;
           mbar_arrive_expect_tx(BAR(QFULL), one ? bytes : 2 * bytes);
+#pragma unroll 1
           for (int s = 0; s < (one ? 1 : 2); ++s)
 #pragma unroll
             for (int cb = 0; cb < C::NB; ++cb)
@@ -292,6 +297,7 @@ k_attn_tc(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUten
       __syncwarp();
     } else if (warp == C::WARP_KV) {
       // ---------------- K and V tiles, page by page: lane i sends page i of the tile
+      const int page_log2 = 31 - __clz(cv.page), page_mask = cv.page - 1;   // a power of two
       const int box = cv.page < BN ? cv.page : BN, boxes = BN / box;
       uint32_t idx = 0, sent = 0;
       bool ok = true;
@@ -310,7 +316,7 @@ k_attn_tc(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUten
         auto page_row = [&](int t) -> int {
           const int kt = t < n_anchor ? t : first + (t - n_anchor), j = kt * BN + lane * box;
           if (lane >= boxes || !(j < anc || (j < end && j + box > lo))) return -1;
-          const int id = __ldg(row_of + j / cv.page);
+          const int id = __ldg(row_of + (j >> page_log2));
           return id >= 0 && id < cv.pages ? id * g.Hk + h : -2;
         };
         int row = page_row(t0);
@@ -318,7 +324,7 @@ k_attn_tc(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUten
           const int here = row;
           if (t + 1 < n) row = page_row(t0 + t + 1);
           const int kt = t0 + t < n_anchor ? t0 + t : first + (t0 + t - n_anchor);
-          const int off = (kt * BN + lane * box) % cv.page;
+          const int off = (kt * BN + lane * box) & page_mask;
           const uint32_t absent = __ballot_sync(0xffffffffu, here == -2);
 #pragma unroll
           for (int v = 0; v < 2; ++v) {
@@ -347,15 +353,14 @@ k_attn_tc(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUten
       }
       __syncwarp();
     } else {
-      // ---------------- MMA issuers, one warp a turn.  A key tile's scores are
-      // taken in halves of 64 keys, so that one half's are computed while the
-      // softmax works on the other: P V of a half, then the next tile's scores
-      // into its place.  An issuing warp spends as long again on waits and
-      // commits as its products take; two of them fill each other's gaps (one
-      // warp for both turns kept the tensor cores busy 45% of the time).  The
-      // whole warp walks the units, so that addresses stay in uniform
-      // registers, and one lane issues.
-      constexpr uint32_t kIdQK = idesc_bf16(128, 64, 0, 0);   // both K-major
+      // ---------------- MMA issuers, one warp a turn: P V of a unit (a key tile
+      // of the turn's rows) as its P comes, then the next unit's scores over S
+      // and P.  An issuing warp spends as long again on waits and commits as
+      // its products take; two of them fill each other's gaps (one warp for
+      // both turns kept the tensor cores busy 45% of the time).  The whole warp
+      // walks the units, so that addresses stay in uniform registers, and one
+      // lane issues.
+      constexpr uint32_t kIdQK = idesc_bf16(128, BN, 0, 0);   // both K-major
       constexpr uint32_t kIdPV = idesc_bf16(128, D, 0, 1);    // V: channels contiguous
       const int tn = __shfl_sync(0xffffffffu, warp, 0) - C::WARP_MMA;
       const uint32_t k_lo = desc_lo(sbase + C::OFF_KV, 16), v_lo = desc_lo(sbase + C::OFF_KV, C::BLK);
@@ -374,33 +379,39 @@ k_attn_tc(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUten
         }
       };
       // the unit whose scores are issued and whose product with V is not
-      bool due = false, due_first = false;
+      bool due = false, due_first = false, due_last = false;   // ... of this turn in its item
       uint32_t due_stage = 0, due_phase = 0;
-      auto pv = [&](int half) -> bool {
-        if (half == 0) {
+      // its product with V, in two parts as P comes: keys 0-63, 64-127
+      auto pv = [&](int part) -> bool {
+        if (part == 0) {
           if (!wait(KVFULL + due_stage, due_phase)) return false;
           if (due_first && !wait(OFREE + tn, begun++ ^ 1u)) return false;   // the output of the last item has been read
         }
-        if (!wait(PFULL + 2 * tn + half, units)) return false;
+        if (!wait(PFULL + 2 * tn + part, units)) return false;
         tc_fence_after();
         if (leader) {
-          const uint32_t vb = v_lo + due_stage * (C::TILE >> 4) + (uint32_t)half * (4 * 2048u >> 4);
-          const uint32_t pa = tS + 64u * half;
+          const uint32_t vb = v_lo + due_stage * (C::TILE >> 4);
 #pragma unroll
-          for (int ks = 0; ks < 4; ++ks)
-            mma_ts(tO, pa + 8u * ks, vb + (uint32_t)ks * (2048u >> 4), kIdPV, !(due_first && half == 0 && ks == 0));
-          mma_commit(BAR(ODONE + 2 * tn + half));
-          if (half == 1) mma_commit(BAR(KVEMPTY + due_stage));
+          for (int ks = 4 * part; ks < 4 * part + 4; ++ks)
+              mma_ts(tO, tS + 8u * ks, vb + (uint32_t)ks * (2048u >> 4), kIdPV, !(due_first && ks == 0));
         }
         __syncwarp();
-        if (half == 1) {
-          ++units;
-          due = false;
-        }
         return true;
       };
+      auto pv_done = [&]() {
+        if (leader) {
+          mma_commit(BAR(KVEMPTY + due_stage));
+          if (due_last) mma_commit(BAR(ODONE + tn));
+        }
+        __syncwarp();
+        ++units;
+        due = false;
+      };
       for (int i = 0; ok; ++i) {
-        if (due && !(pv(0) && pv(1))) break;
+        if (due) {
+          if (!(pv(0) && pv(1))) break;
+          pv_done();
+        }
         if (!__all_sync(0xffffffffu, item_ready(i))) break;
         const volatile Item& it = items[i % C::NIT];
         const int n = __shfl_sync(0xffffffffu, it.n, 0), flags = __shfl_sync(0xffffffffu, it.flags, 0);
@@ -415,7 +426,10 @@ k_attn_tc(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUten
         for (int t = 0; t < n; ++t) {
           if (due && !pv(0)) { ok = false; break; }
           if (one) {
-            if (due && !pv(1)) { ok = false; break; }
+            if (due) {
+              if (!pv(1)) { ok = false; break; }
+              pv_done();
+            }
             if ((t & 1) != tn) {   // the other turn's tile: seen and passed over
               for (int v = 0; v < 2 && ok; ++v) {
                 ok = wait(KVFULL + stage, phase);
@@ -426,24 +440,22 @@ k_attn_tc(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUten
               continue;
             }
           }
+          // what the scores need is waited for before the last of P, so that
+          // they follow the product without a gap; the commits come after both
+          if (due) {
+            if (!pv(1)) { ok = false; break; }
+            pv_done();
+          }
           if (!wait(KVFULL + stage, phase)) { ok = false; break; }
           tc_fence_after();
-          const uint32_t kb = k_lo + stage * (C::TILE >> 4);
-#pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            if (half == 1 && due && !pv(1)) { ok = false; break; }
-            if (leader) {
-#pragma unroll
-              for (int ks = 0; ks < D / 16; ++ks) {
-                const uint32_t off = ((uint32_t)(ks >> 2) * C::BLK + (uint32_t)(ks & 3) * 32u) >> 4;
-                mma_ss(tS + 64u * half, q_lo + off, kb + off + (uint32_t)half * (64u * 128u >> 4), kIdQK, ks != 0);
-              }
-              mma_commit(BAR(SFULL + 2 * tn + half));
-            }
-            __syncwarp();
-          }
-          if (!ok) break;
           if (leader) {
+            const uint32_t kb = k_lo + stage * (C::TILE >> 4);
+#pragma unroll
+            for (int ks = 0; ks < D / 16; ++ks) {
+              const uint32_t off = ((uint32_t)(ks >> 2) * C::BLK + (uint32_t)(ks & 3) * 32u) >> 4;
+              mma_ss(tS, q_lo + off, kb + off, kIdQK, ks != 0);
+            }
+            mma_commit(BAR(SFULL + tn));
             mma_commit(BAR(KVEMPTY + stage));
             if (t + 1 == end) mma_commit(BAR(QEMPTY));
           }
@@ -451,6 +463,7 @@ k_attn_tc(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUten
           advance();
           due = true;
           due_first = first;
+          due_last = t + 1 == end;
           due_stage = stage;
           due_phase = phase;
           advance();
@@ -471,7 +484,7 @@ k_attn_tc(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUten
     const uint32_t tS = tmem + lanes + C::T_S + tn * 128u, tO = tmem + lanes + C::T_O + (uint32_t)tn * D;
     const int box = cv.page < BN ? cv.page : BN;
     const int ri = r / g.group;   // token of the tile
-    uint32_t cnt = 0;             // units of this turn so far
+    uint32_t cnt = 0, outs = 0;   // units of this turn so far, items with units
     uint32_t base = 0;            // key tiles before the item
     int merges = 0;               // 64-row halves merged so far
     auto arrive = [&](int bar) {   // the warp's one arrival, after its lanes' TMEM and shared-memory accesses
@@ -487,11 +500,12 @@ k_attn_tc(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUten
     // (4500 cycles for 128 keys of both turns).  Round k of turn 0 follows
     // round k - 1 of turn 1, round k of turn 1 follows round k of turn 0.
     uint32_t rounds = 0;
-    auto exp_begin = [&]() -> bool {
-      if (tn == 0 && rounds == 0) return true;
+    auto exp_begin = [&](bool one) -> bool {
+      if (one || (tn == 0 && rounds == 0)) return true;
       return wait(EXPED + (tn ^ 1) * 4 + (warp & 3), tn ? rounds : rounds - 1u);
     };
-    auto exp_end = [&]() {
+    auto exp_end = [&](bool one) {
+      if (one) return;
       __syncwarp();
       if (lane == 0) mbar_arrive(BAR(EXPED + tn * 4 + (warp & 3)));
       ++rounds;
@@ -514,114 +528,102 @@ k_attn_tc(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUten
       for (int t = one ? tn : 0; ok && t < n; t += one ? 2 : 1, ++cnt, ++done) {
         const int kt = it.t0 + t, na = it.n_anchor;
         const int j0 = (kt < na ? kt : it.first + (kt - na)) * BN;
-        uint32_t absent = 0u;   // pages of the tile that do not exist
-        bool masked = false;    // some row of the warp does not see the whole tile
+        if (!wait(SFULL + tn, cnt)) { ok = false; break; }
+        tc_fence_after();
+        // keys of the tile that no row of the item sees: their values may be
+        // anything (0 x NaN would reach the sums), so they become zeros
+        if (!(j0 + BN <= it.anc || (j0 >= it.lo && j0 + BN <= it.end))) {
+          const uint32_t k = 2u * (base + (uint32_t)t) + 1u, s = k % C::NST;
+          if (!wait(KVFULL + s, k / C::NST)) { ok = false; break; }
+          const int j = j0 + r;
+          if (!(j < it.anc || (j >= it.lo && j < it.end))) {
+            const uint32_t at = sbase + C::OFF_KV + s * C::TILE + (uint32_t)r * 128u;
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          if (!wait(SFULL + 2 * tn + half, cnt)) { ok = false; break; }
-          tc_fence_after();
-          // keys of the tile that no row of the item sees: their values may be
-          // anything (0 x NaN would reach the sums), so they become zeros
-          if (half == 0 && !(j0 + BN <= it.anc || (j0 >= it.lo && j0 + BN <= it.end))) {
-            const uint32_t k = 2u * (base + (uint32_t)t) + 1u, s = k % C::NST;
-            if (!wait(KVFULL + s, k / C::NST)) { ok = false; break; }
-            const int j = j0 + r;
-            if (!(j < it.anc || (j >= it.lo && j < it.end))) {
-              const uint32_t at = sbase + C::OFF_KV + s * C::TILE + (uint32_t)r * 128u;
+            for (int cb = 0; cb < C::NB; ++cb)
 #pragma unroll
-              for (int cb = 0; cb < C::NB; ++cb)
-#pragma unroll
-                for (int c = 0; c < 8; ++c) st_shared_v4(at + cb * C::BLK + 16u * c, make_uint4(0u, 0u, 0u, 0u));
-            }
-            fence_proxy_async_smem();
+              for (int c = 0; c < 8; ++c) st_shared_v4(at + cb * C::BLK + 16u * c, make_uint4(0u, 0u, 0u, 0u));
           }
-          if (!busy) {
-            if (!exp_begin()) { ok = false; break; }
-            exp_end();
-            arrive(PFULL + 2 * tn + half);
-            continue;
-          }
-          const uint32_t tSh = tS + 64u * half;
-          const int jh = j0 + 64 * half;
-          uint32_t v[2][32];
-          tmem_ld32(tSh, v[0]);
-          tmem_ld32(tSh + 32u, v[1]);
-          if (half == 0) {
-            absent = gone[(base + (uint32_t)t) % C::NGONE];
-            const bool all = !valid || j0 + BN <= sp.anc || (j0 >= sp.lo && j0 + BN <= sp.end);
-            masked = !__all_sync(0xffffffffu, all && absent == 0u);
-          }
-          tmem_wait_ld();
-          if (masked) {
+          fence_proxy_async_smem();
+        }
+        if (!busy) {
+          if (!exp_begin(one)) { ok = false; break; }
+          exp_end(one);
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              const uint32_t see = seen_word(sp, jh + 32 * c) & ~absent_word(absent, 2 * half + c, box);
+          for (int p = 0; p < 2; ++p) arrive(PFULL + 2 * tn + p);
+          continue;
+        }
+        uint32_t v[4][32];
 #pragma unroll
-              for (int e = 0; e < 32; ++e)
-                if (!((see >> e) & 1u)) v[c][e] = 0xff800000u;
-            }
-          }
-          float mx[4];
+        for (int c = 0; c < 4; ++c) tmem_ld32(tS + 32u * c, v[c]);
+        const uint32_t absent = gone[(base + (uint32_t)t) % C::NGONE];   // pages of the tile that do not exist
+        const bool all = !valid || j0 + BN <= sp.anc || (j0 >= sp.lo && j0 + BN <= sp.end);
+        const bool masked = !__all_sync(0xffffffffu, all && absent == 0u);
+        tmem_wait_ld();
+        if (masked) {
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
-            const uint32_t* x = v[c >> 1] + 16 * (c & 1);
-            mx[c] = __uint_as_float(x[0]);
+            const uint32_t see = seen_word(sp, j0 + 32 * c) & ~absent_word(absent, c, box);
 #pragma unroll
-            for (int e = 1; e < 15; e += 2) mx[c] = fmaxf(fmaxf(mx[c], __uint_as_float(x[e])), __uint_as_float(x[e + 1]));
-            mx[c] = fmaxf(mx[c], __uint_as_float(x[15]));
+            for (int e = 0; e < 32; ++e)
+              if (!((see >> e) & 1u)) v[c][e] = 0xff800000u;
           }
-          const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-          // a row's first keys set its maximum; later it moves when outgrown
-          const bool grow = m != neg_inf() && (top - m) * c2 > 8.f;
-          if (__any_sync(0xffffffffu, grow)) {
-            const float alpha = grow ? ex2((m - top) * c2) : 1.f;
-            l *= alpha;
-            if (!wait(ODONE + 2 * tn + (half ^ 1), half ? cnt : cnt - 1u)) { ok = false; break; }
-            tc_fence_after();
+        }
+        float mx[8];
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          const uint32_t* x = v[c >> 1] + 16 * (c & 1);
+          mx[c] = __uint_as_float(x[0]);
+#pragma unroll
+          for (int e = 1; e < 15; e += 2) mx[c] = fmaxf(fmaxf(mx[c], __uint_as_float(x[e])), __uint_as_float(x[e + 1]));
+          mx[c] = fmaxf(mx[c], __uint_as_float(x[15]));
+        }
+        const float top = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7])));
+        // a row's first keys set its maximum; later it moves when outgrown (the
+        // products so far are complete: the scores came after them)
+        const bool grow = m != neg_inf() && (top - m) * c2 > 8.f;
+        if (__any_sync(0xffffffffu, grow)) {
+          const float alpha = grow ? ex2((m - top) * c2) : 1.f;
+          l *= alpha;
 #pragma unroll 1
-            for (int c = 0; c < D / 16; ++c) {
-              uint32_t o[16];
-              tmem_ld16(tO + 16u * c, o);
-              tmem_wait_ld();
+          for (int c = 0; c < D / 16; ++c) {
+            uint32_t o[16];
+            tmem_ld16(tO + 16u * c, o);
+            tmem_wait_ld();
 #pragma unroll
-              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-              tmem_st16(tO + 16u * c, o);
-            }
+            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+            tmem_st16(tO + 16u * c, o);
           }
-          if (grow || m == neg_inf()) m = top;
-          const float nb = m == neg_inf() ? 0.f : -m * c2;
-          if (!exp_begin()) { ok = false; break; }
-          float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            uint32_t p[16];
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              // scalar, not paired, arithmetic: with one warp of an SM quarter at
-              // work 64 keys take 592 cycles instead of 765 (512 of the XU pipe)
-              const float a = ex2(fmaf(__uint_as_float(v[c][2 * e]), c2, nb));
-              const float b = ex2(fmaf(__uint_as_float(v[c][2 * e + 1]), c2, nb));
-              sum[2 * (e & 1)] += a;
-              sum[2 * (e & 1) + 1] += b;
-              p[e] = pack_bf16(a, b);
-            }
-            tmem_st16(tSh + 16u * c, p);
-          }
-          exp_end();
-          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-          tmem_wait_st();
-          arrive(PFULL + 2 * tn + half);
         }
+        if (grow || m == neg_inf()) m = top;
+        const float nb = m == neg_inf() ? 0.f : -m * c2;
+        if (!exp_begin(one)) { ok = false; break; }
+        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t p[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            // scalar, not paired, arithmetic: with one warp of an SM quarter at
+            // work 64 keys take 592 cycles instead of 765 (512 of the XU pipe)
+            const float a = ex2(fmaf(__uint_as_float(v[c][2 * e]), c2, nb));
+            const float b = ex2(fmaf(__uint_as_float(v[c][2 * e + 1]), c2, nb));
+            sum[2 * (e & 1)] += a;
+            sum[2 * (e & 1) + 1] += b;
+            p[e] = pack_bf16(a, b);
+          }
+          tmem_st16(tS + 16u * c, p);
+          if (c == 3) exp_end(one);
+          if (c & 1) {   // a half of P is there for its product with V
+            tmem_wait_st();
+            arrive(PFULL + 2 * tn + (c >> 1));
+          }
+        }
+        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
       }
-      if (one && tn == 1 && (n & 1))   // turn 0 has one unit more
-        for (int half = 0; ok && half < 2; ++half) {
-          ok = exp_begin();
-          exp_end();
-        }
       if (!ok) break;
       base += (uint32_t)n;
       if (done > 0) {   // the turn's last product
-        if (!wait(ODONE + 2 * tn + 1, cnt - 1u)) break;
+        if (!wait(ODONE + tn, outs++)) break;
         tc_fence_after();
       }
       // rows of a single tile: turn 1 hands its sums to turn 0 in shared

@@ -385,8 +385,8 @@ VDA_API int vda_qk_norm_rope_backward(const vda_qk_grad_args* args, void* worksp
  * q_start[0] and from q_start[B] on are left as they were.
  * q, out, lse: rows as described above; lse [N, Hq] float32 contiguous or NULL.
  * S, the softmax's maximum and sum and the output sums are float32; on the
- * tensor cores (bf16, d = 64 or 128, page_size a power of two from 8 to 128 or a
- * multiple of 128) the weights are rounded to bf16 before their product with
+ * tensor cores (bf16, d = 64 or 128, page_size a power of two from 8 on) the
+ * weights are rounded to bf16 before their product with
  * V, their sum is not.  Other types and sizes run on a SIMT kernel in float32.
  * Supported: d in {16, 32, 64, 128}; Hq / Hk up to 128 on the tensor cores,
  * 64 elsewhere; pages * Hk < 2^31.  The lengths and the table are read on the
