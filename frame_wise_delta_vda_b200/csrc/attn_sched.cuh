@@ -6,7 +6,10 @@
 // New tokens and cached keys differ from sequence to sequence and are known
 // on the device only.  All items' key tiles, in the order sequence, KV head,
 // run of tokens, form one line of W tiles; CTA g of G takes the tiles
-// [W g / G, W (g + 1) / G) or so, which may begin and end inside an item.  The parts
+// [W g / G, W (g + 1) / G) or so, which may begin and end inside an item.  Every
+// item counts Geom::item_cost tiles more, before its own, for what it costs to begin and
+// end one (without it, the CTAs with the short sequences of a ragged batch end a
+// third later than the others).  The parts
 // of an item that several CTAs took are joined afterwards (their running
 // maximum and sum say how).  So long and short sequences, one token or
 // thousands of them, load every SM alike, without a plan made on the host.
@@ -36,6 +39,7 @@ struct Geom {
   int tpi;              // tokens of an item
   int max_keys;         // places in a row of the block table
   int block, window, anchors;
+  int item_cost;        // what an item costs besides its key tiles, in tiles
 };
 
 VDA_HD int imin(int a, int b) { return a < b ? a : b; }
@@ -128,15 +132,15 @@ __device__ __noinline__ int item_tiles(const Geom& g, int n, int len, int r) {
   s.n = n;
   s.len = len;
   const int i0 = r * g.tpi;
-  return tiles_of<BN>(g, s, i0, imin(g.tpi, n - i0)).count;
+  return tiles_of<BN>(g, s, i0, imin(g.tpi, n - i0)).count + g.item_cost;
 }
 
 // Where a CTA's share begins.
 struct Plan {
-  int W, w0, w1;         // all tiles; this share
+  int W, w0, w1;         // all items' costs; this share
   int shares;            // CTAs with work
   int b, h, r;           // item in which the share begins
-  int t;                 // tiles of that item before it
+  int t;                 // of that item's cost, what lies before it
 };
 
 constexpr int kSerialItems = 4;   // longer sequences are counted by the whole warp
@@ -245,16 +249,17 @@ __device__ __forceinline__ Plan plan_share(const Geom& g, int cta, int ctas, int
 template <int BN>
 struct Walk {
   const Geom* g;
-  int left;              // tiles of the share from this item's on
+  int left;              // cost of the share from this item's part on
   int b, h, r;
   Seq s;
   int i0, ntok;          // tokens [i0, i0 + ntok) of the sequence
   Tiles tiles;
-  int t0, t1;            // this share's tiles of the item
+  int c0, c1;            // this share's part of the item's cost
+  int t0, t1;            // its key tiles
   bool live;
 
   __device__ __forceinline__ Walk(const Geom& geom, const Plan& p)
-      : g(&geom), left(p.w1 - p.w0), b(p.b), h(p.h), r(p.r), t0(p.t) {
+      : g(&geom), left(p.w1 - p.w0), b(p.b), h(p.h), r(p.r), c0(p.t) {
     live = left > 0;
     if (!live) return;
     s = load_seq(*g, b);
@@ -264,27 +269,35 @@ struct Walk {
     i0 = r * g->tpi;
     ntok = imin(g->tpi, s.n - i0);
     tiles = tiles_of<BN>(*g, s, i0, ntok);
-    t1 = left < tiles.count - t0 ? t0 + left : tiles.count;
+    const int all = tiles.count + g->item_cost;
+    c1 = left < all - c0 ? c0 + left : all;
+    t0 = imax(0, c0 - g->item_cost);
+    t1 = imax(0, c1 - g->item_cost);
+    live = t1 > t0;   // a share that ends before the item's first tile leaves it to the next one
   }
   __device__ __forceinline__ int n() const { return t1 - t0; }
   __device__ __forceinline__ bool whole() const { return t0 == 0 && t1 == tiles.count; }
+  // of an item that begins in share `cta` and goes on: the shares with a part of it
+  __device__ __forceinline__ int parts(const Plan& p, int cta) const {
+    return share_of(p.W, p.w1 - (c1 - c0) - c0 + tiles.count + g->item_cost - 1, p.shares) - cta + 1;
+  }
   __device__ __forceinline__ bool next() {
-    left -= n();
+    left -= c1 - c0;
     live = left > 0;
     if (!live) return false;
-    t0 = 0;
+    c0 = 0;
     if (++r == items_of(*g, s.n)) {
       r = 0;
       if (++h == g->Hk) {
         h = 0;
-        do {   // tiles are left, so a sequence with new tokens follows
+        do {   // some is left, so a sequence with new tokens follows
           if (++b >= g->B) return live = false;
           s = load_seq(*g, b);
         } while (s.n == 0);
       }
     }
     item();
-    return true;
+    return live;
   }
 };
 

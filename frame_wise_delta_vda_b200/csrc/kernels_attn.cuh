@@ -15,6 +15,8 @@
 #include <cuda_bf16.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "attn_sched.cuh"
 #include "common.cuh"
 #include "tc_ptx.cuh"
@@ -104,8 +106,10 @@ k_attn_simt(const T* __restrict__ q, int64_t q_ts, int64_t q_hs, const T* __rest
   Meta meta{0, 0, 0, 0};
   for (Walk<BN> w(g, pl); w.live; w.next()) {
     const int rows = w.ntok * g.group, tok0 = w.s.q0 + w.i0;
-    for (int e = tid; e < BM * V4; e += C::THREADS) {
-      const int r = e / V4, v = e - r * V4;
+#pragma unroll
+    for (int k = 0; k < (BM * V4 + C::THREADS - 1) / C::THREADS; ++k) {
+      const int e = tid + k * C::THREADS, r = e / V4, v = e - r * V4;
+      if (r >= BM) break;
       float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
       if (r < rows) x = load4(q + (int64_t)(tok0 + r / g.group) * q_ts + (int64_t)(w.h * g.group + r % g.group) * q_hs + 4 * v);
       *reinterpret_cast<float4*>(Qs + r * D + 4 * v) = x;
@@ -124,8 +128,10 @@ k_attn_simt(const T* __restrict__ q, int64_t q_ts, int64_t q_hs, const T* __rest
     }
     for (int t = w.t0; t < w.t1; ++t) {
       const int j0 = key_tile(w.tiles, t) * BN;
-      for (int e = tid; e < BN * V4; e += C::THREADS) {
-        const int r = e / V4, v = e - r * V4, j = j0 + r;
+#pragma unroll
+      for (int k = 0; k < (BN * V4 + C::THREADS - 1) / C::THREADS; ++k) {   // unrolled: the loads overlap
+        const int e = tid + k * C::THREADS, r = e / V4, v = e - r * V4, j = j0 + r;
+        if (r >= BN) break;
         // keys that no row of the item sees read as zeros: what lies there may be anything
         float4 kx = make_float4(0.f, 0.f, 0.f, 0.f), vx = kx;
         int id = -1;
@@ -222,8 +228,7 @@ k_attn_simt(const T* __restrict__ q, int64_t q_ts, int64_t q_hs, const T* __rest
     const bool whole = w.whole();
     const int slot = w.t0 > 0 ? 0 : 1;
     if (!whole && slot == 1) {   // begun here, continued in later shares
-      const int start = pl.w1 - w.n();
-      meta.parts = share_of(pl.W, start + w.tiles.count - 1, pl.shares) - (int)blockIdx.x + 1;
+      meta.parts = w.parts(pl, blockIdx.x);
       meta.tok0 = tok0;
       meta.h = w.h;
       meta.rows = rows;
@@ -326,6 +331,8 @@ k_attn_join(Parts parts, OutView<T> ov, int group) {
 // ------------------------------------------------------------------- host
 inline size_t align256(size_t x) { return (x + 255) / 256 * 256; }
 
+constexpr int kTcItemCost = 3;
+
 struct AttnPlan {
   bool tc;
   int ctas, rows, tpi;     // CTAs, rows of a part, tokens of an item
@@ -374,6 +381,7 @@ inline Geom geom_of(const vda_attn_args& a, const AttnPlan& p) {
   const long long keys = (long long)a.max_pages * a.page_size;
   g.max_keys = keys > 2147483647LL ? 2147483647 : (int)keys;
   g.block = a.block; g.window = a.window_blocks; g.anchors = a.anchors;
+  g.item_cost = p.tc ? kTcItemCost : 0;
   return g;
 }
 
@@ -393,12 +401,24 @@ int launch_join(const AttnPlan& p, const Parts& parts, const OutView<T>& ov, int
                         parts, ov, group);
 }
 
+// Shared memory of a kernel, set the first time that a device runs it.
+template <typename K>
+bool allow_smem(K kernel, size_t bytes, std::atomic<bool> (&done)[64]) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return false;
+  const bool known = dev >= 0 && dev < 64;
+  if (known && done[dev].load(std::memory_order_relaxed)) return true;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) != cudaSuccess) return false;
+  if (known) done[dev].store(true, std::memory_order_relaxed);
+  return true;
+}
+
 template <typename T, int D, int BM>
 int launch_simt(const vda_attn_args& a, const AttnPlan& p, char* ws, float c2) {
   using C = SimtCfg<D, BM>;
   auto kernel = k_attn_simt<T, D, BM>;
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM) != cudaSuccess)
-    return VDA_ERR_CUDA;
+  static std::atomic<bool> set[64];
+  if (!allow_smem(kernel, C::SMEM, set)) return VDA_ERR_CUDA;
   const Geom g = geom_of(a, p);
   const OutView<T> ov = out_of<T>(a);
   const Parts parts = parts_of(ws, p);

@@ -262,7 +262,7 @@ k_attn_tc(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUten
               it.flags = (single ? kSingle : 0) | (w.whole() ? kWhole : 0) | (last ? kLast : 0) |
                          ((single && w.n() > 1 ? (rows > 64 ? 2 : 1) : 0) << kHalfShift);
               if (last) {
-                meta.parts = share_of(plan.W, plan.w1 - w.n() + w.tiles.count - 1, plan.shares) - (int)blockIdx.x + 1;
+                meta.parts = w.parts(plan, blockIdx.x);
                 meta.tok0 = w.s.q0 + w.i0;
                 meta.h = w.h;
                 meta.rows = rows;
@@ -762,8 +762,8 @@ int launch_attn_tc(const vda_attn_args& a, const AttnPlan& p, char* ws, float c2
       !tc::encode_bf16_3d(&tmV, a.v_cache, (uint64_t)a.page_size, heads, box, D))
     return VDA_ERR_CUDA;
   auto kernel = k_attn_tc<D>;
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM) != cudaSuccess)
-    return VDA_ERR_CUDA;
+  static std::atomic<bool> set[64];
+  if (!allow_smem(kernel, C::SMEM, set)) return VDA_ERR_CUDA;
   const OutView<__nv_bfloat16> ov = out_of<__nv_bfloat16>(a);
   const Parts parts = parts_of(ws, p);
   const CacheView cv{a.block_table, a.table_stride, a.pages, a.page_size};

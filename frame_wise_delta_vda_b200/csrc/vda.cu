@@ -540,7 +540,7 @@ int vda_paged_attention(const vda_attn_args* a, void* workspace, size_t workspac
       vda::attn::make_attn_plan(a->dtype, a->Hq, a->Hk, a->d, a->page_size, a->N, a->B, vda::tc::num_sms());
   // every CTA's share is counted in 32 bits
   const double items = ((double)a->N / p.tpi + a->B) * a->Hk, keys = (double)a->max_pages * a->page_size;
-  if (items * (keys / 64 + 2) > 2147483647.0) return VDA_ERR_UNSUPPORTED;
+  if (items * (keys / 64 + 2 + vda::attn::kTcItemCost) > 2147483647.0) return VDA_ERR_UNSUPPORTED;
   // the tensor map of q steps over at least 16 and less than 2^40 bytes
   if (p.tc && ((a->N > 1 && (a->q.token_stride < 8 || a->q.token_stride >= (1LL << 39))) ||
                (a->Hq > 1 && (a->q.head_stride < 8 || a->q.head_stride >= (1LL << 39)))))
