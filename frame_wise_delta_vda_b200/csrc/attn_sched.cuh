@@ -182,8 +182,9 @@ __device__ __noinline__ int prefix_sum(int v, int lane) {   // inclusive, over t
 }
 
 // One warp finds share `cta` of `ctas`.  The host bounds W below 2^31 for
-// ascending q_start; overlapping sequences may pass it and get wrong results,
-// within the tensors all the same.
+// ascending q_start, and any one sequence's tiles whatever it holds;
+// overlapping sequences may pass it together and get wrong results, but the
+// clamps here and in Walk keep them within the tensors.
 template <int BN>
 __device__ __forceinline__ Plan plan_share(const Geom& g, int cta, int ctas, int lane) {
   const int chunks = (g.B + 31) / 32;
@@ -214,8 +215,9 @@ __device__ __forceinline__ Plan plan_share(const Geom& g, int cta, int ctas, int
     const int l = __ffs(hit) - 1;
     const int per_head = __shfl_sync(0xffffffffu, w, l);
     rest -= __shfl_sync(0xffffffffu, upto, l) - per_head * g.Hk;
+    rest = imax(0, rest);
     p.b = c * 32 + l;
-    p.h = rest / per_head;
+    p.h = imin(rest / per_head, g.Hk - 1);
     rest -= p.h * per_head;
     // the run of tokens that holds tile `rest` of this head
     const Seq s = load_seq(g, p.b);
@@ -279,7 +281,8 @@ struct Walk {
   __device__ __forceinline__ bool whole() const { return t0 == 0 && t1 == tiles.count; }
   // of an item that begins in share `cta` and goes on: the shares with a part of it
   __device__ __forceinline__ int parts(const Plan& p, int cta) const {
-    return share_of(p.W, p.w1 - (c1 - c0) - c0 + tiles.count + g->item_cost - 1, p.shares) - cta + 1;
+    const int last = share_of(p.W, p.w1 - (c1 - c0) - c0 + tiles.count + g->item_cost - 1, p.shares);
+    return imin(last, p.shares - 1) - cta + 1;
   }
   __device__ __forceinline__ bool next() {
     left -= c1 - c0;

@@ -159,3 +159,53 @@ def test_paged_attention_workspace(L):
     assert L.vda_paged_attention(None, P, 1) == INVALID
     z = VdaRows()
     assert L.vda_paged_attention(ctypes.byref(attn_args(N=0, q=z, out=z)), None, 0) == 0
+
+
+def test_binding_refuses_host_tensors_and_wrong_shapes():
+    torch = pytest.importorskip("torch")
+    from frame_wise_delta_vda_b200 import api
+    q, k = torch.zeros(3, 4, 64), torch.zeros(3, 2, 64)
+    with pytest.raises(ValueError, match="CUDA"):
+        api.vda_qk_norm_rope(q, k)
+    with pytest.raises(ValueError, match="CUDA"):
+        api.vda_qk_norm_rope_backward(q, k, q, k)
+    with pytest.raises(ValueError, match="heads"):
+        api.vda_qk_norm_rope(q[0], k)
+    with pytest.raises(ValueError, match="CUDA"):
+        api.vda_paged_attention(q, None, None, None, None, None)
+    with pytest.raises(ValueError, match="Hq"):
+        api.vda_paged_attention(q[0], None, None, None, None, None)
+
+
+def test_rope_frequencies():
+    torch = pytest.importorskip("torch")
+    from frame_wise_delta_vda_b200 import api
+    f, a = api.rope_frequencies(16, 100.0, [4, 2, 2], device="cpu")
+    assert f.dtype == torch.float64 and a.dtype == torch.int32
+    assert a.tolist() == [0, 0, 0, 0, 1, 1, 2, 2]
+    assert f.tolist() == pytest.approx([1, 100 ** -0.25, 0.1, 100 ** -0.75, 1, 0.1, 1, 0.1])
+    assert api.rope_frequencies(8, device="cpu")[0].tolist() == pytest.approx([1, 0.1, 0.01, 0.001])
+    for bad in ((7, None), (16, [4, 2]), (16, [10, -2])):
+        with pytest.raises(ValueError):
+            api.rope_frequencies(bad[0], sections=bad[1], device="cpu")
+
+
+@pytest.mark.parametrize("mirror,pack", [(VdaQkArgs, _lib.pack_qk), (VdaQkGradArgs, _lib.pack_qk_grad),
+                                         (VdaAttnArgs, _lib.pack_attn)])
+def test_packed_arguments_are_the_struct(mirror, pack):
+    """Every field, packed in order, is found in the struct's place."""
+    leaves = []
+
+    def fill(m, base):
+        for name, t in m._fields_:
+            if issubclass(t, ctypes.Structure):
+                fill(t, base + getattr(m, name).offset)
+            else:
+                leaves.append((base + getattr(m, name).offset, t))
+
+    fill(mirror, 0)
+    values = [float(i) if t is ctypes.c_float else i + 1 for i, (_, t) in enumerate(leaves)]
+    raw = pack(*values)
+    assert len(raw) == ctypes.sizeof(mirror)
+    for v, (off, t) in zip(values, leaves):
+        assert (t.from_buffer_copy(raw, off).value or 0) == v
