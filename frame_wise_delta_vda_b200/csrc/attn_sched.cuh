@@ -4,8 +4,8 @@
 // arithmetic is tested without a GPU.
 //
 // New tokens and cached keys differ from sequence to sequence and are known
-// on the device only.  All items' key tiles, in the order sequence, KV head,
-// run of tokens, form one line of W tiles; CTA g of G takes the tiles
+// on the device only.  All items' key tiles, in the order sequence, run of
+// tokens, KV head, form one line of W tiles; CTA g of G takes the tiles
 // [W g / G, W (g + 1) / G) or so, which may begin and end inside an item.  Every
 // item counts Geom::item_cost tiles more, before its own, for what it costs to begin and
 // end one (without it, the CTAs with the short sequences of a ragged batch end a
@@ -122,19 +122,6 @@ __device__ __forceinline__ Seq load_seq(const Geom& g, int b) {
   return make_seq(g, __ldg(g.q_start + b), __ldg(g.q_start + b + 1), __ldg(g.kv_len + b));
 }
 
-// What follows runs once a CTA, on code that no cache holds yet: a fetch of
-// instructions costs as much as a load of data, so it is kept small (one copy of
-// the counting, called) rather than unrolled.
-template <int BN>
-__device__ __noinline__ int item_tiles(const Geom& g, int n, int len, int r) {
-  Seq s;
-  s.q0 = 0;
-  s.n = n;
-  s.len = len;
-  const int i0 = r * g.tpi;
-  return tiles_of<BN>(g, s, i0, imin(g.tpi, n - i0)).count + g.item_cost;
-}
-
 // Where a CTA's share begins.
 struct Plan {
   int W, w0, w1;         // all items' costs; this share
@@ -143,106 +130,82 @@ struct Plan {
   int t;                 // of that item's cost, what lies before it
 };
 
-constexpr int kSerialItems = 4;   // longer sequences are counted by the whole warp
-
-// One head's tiles of sequences 32 c .. 32 c + 31, one a lane.
-template <int BN>
-__device__ __noinline__ int chunk_tiles(const Geom& g, int c, int lane) {
-  const int b = c * 32 + lane;
-  Seq s{0, 0, 0};
-  if (b < g.B) s = load_seq(g, b);
-  const int n = items_of(g, s.n);
-  const bool longer = n > kSerialItems;
-  int w = 0;
-#pragma unroll 1
-  for (int r = 0; r < n && !longer; ++r) w += item_tiles<BN>(g, s.n, s.len, r);
-  __syncwarp();
-  unsigned todo = __ballot_sync(0xffffffffu, longer);
-#pragma unroll 1
-  while (todo) {
-    const int l = __ffs(todo) - 1;
-    todo &= todo - 1;
-    const int sn = __shfl_sync(0xffffffffu, s.n, l), sl = __shfl_sync(0xffffffffu, s.len, l);
-    int v = 0;
-#pragma unroll 1
-    for (int r = lane; r < items_of(g, sn); r += 32) v += item_tiles<BN>(g, sn, sl, r);
-    v = __reduce_add_sync(0xffffffffu, v);
-    if (lane == l) w = v;
-  }
-  return w;
-}
-
-__device__ __noinline__ int prefix_sum(int v, int lane) {   // inclusive, over the warp
-#pragma unroll
-  for (int off = 1; off < 32; off <<= 1) {
-    const int u = __shfl_up_sync(0xffffffffu, v, off);
-    if (lane >= off) v += u;
-  }
-  return v;
-}
-
-// One warp finds share `cta` of `ctas`.  The host bounds W below 2^31 for
-// ascending q_start, and any one sequence's tiles whatever it holds;
-// overlapping sequences may pass it together and get wrong results, but the
-// clamps here and in Walk keep them within the tensors.
+// One warp finds share `cta` of `ctas`.  It walks the runs of tokens of all
+// sequences twice, 32 at a time: for their total cost, and for the run in which
+// the share begins.  This runs once a CTA, on code that no cache holds yet,
+// where a fetch of instructions costs as much as a load of data: one small loop
+// body for both passes.  (Counted by sequences, with a branch for long ones and
+// called functions, it took 4 to 11 us.)
+//
+// The host bounds W below 2^31 for ascending q_start, and any one sequence's
+// tiles whatever it holds; overlapping sequences may pass it together and get
+// wrong results, but the clamps here and in Walk keep them within the tensors.
 template <int BN>
 __device__ __forceinline__ Plan plan_share(const Geom& g, int cta, int ctas, int lane) {
-  const int chunks = (g.B + 31) / 32;
-  int total = 0, kept = 0;   // kept: the first chunk's tiles, all there are up to 32 sequences
-#pragma unroll 1
-  for (int c = 0; c < chunks; ++c) {
-    const int w = chunk_tiles<BN>(g, c, lane);
-    if (c == 0) kept = w;
-    total += w;
-  }
   Plan p;
-  p.W = imax(0, __reduce_add_sync(0xffffffffu, total) * g.Hk);
-  p.w0 = p.w1 = p.b = p.h = p.r = p.t = 0;
-  p.shares = imin(p.W, ctas);
-  if (cta >= p.shares) return p;
-  p.w0 = share_begin(p.W, cta, p.shares);
-  p.w1 = share_begin(p.W, cta + 1, p.shares);
-  int rest = p.w0;   // tiles still to pass
+  p.W = p.w0 = p.w1 = p.shares = p.b = p.h = p.r = p.t = 0;
+  int sum = 0, rest = 0;   // pass 0: this lane's costs; pass 1: cost still to pass
 #pragma unroll 1
-  for (int c = 0; c < chunks; ++c) {
-    const int w = c == 0 ? kept : chunk_tiles<BN>(g, c, lane);
-    const int upto = prefix_sum(w * g.Hk, lane);
-    const unsigned hit = __ballot_sync(0xffffffffu, upto > rest);
-    if (!hit) {
-      rest -= __shfl_sync(0xffffffffu, upto, 31);
-      continue;
-    }
-    const int l = __ffs(hit) - 1;
-    const int per_head = __shfl_sync(0xffffffffu, w, l);
-    rest -= __shfl_sync(0xffffffffu, upto, l) - per_head * g.Hk;
-    rest = imax(0, rest);
-    p.b = c * 32 + l;
-    p.h = imin(rest / per_head, g.Hk - 1);
-    rest -= p.h * per_head;
-    // the run of tokens that holds tile `rest` of this head
-    const Seq s = load_seq(g, p.b);
-    const int n = items_of(g, s.n);
-    if (n == 1) {
-      p.t = rest;
-      break;
-    }
+  for (int pass = 0; pass < 2; ++pass) {
 #pragma unroll 1
-    for (int r0 = 0; r0 < n; r0 += 32) {
-      const int r = r0 + lane;
-      const int k = r < n ? item_tiles<BN>(g, s.n, s.len, r) : 0;
-      __syncwarp();
-      const int pre = prefix_sum(k, lane);
-      const unsigned at = __ballot_sync(0xffffffffu, pre > rest);
-      if (at) {
-        const int rl = __ffs(at) - 1;
-        p.r = r0 + rl;
-        p.t = rest - (__shfl_sync(0xffffffffu, pre, rl) - __shfl_sync(0xffffffffu, k, rl));
-        break;
+    for (int b0 = 0; b0 < g.B; b0 += 32) {
+      Seq s{0, 0, 0};
+      if (b0 + lane < g.B) s = load_seq(g, b0 + lane);
+      const int runs = items_of(g, s.n);
+      int upto = runs;   // runs of the sequences up to this lane's
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, upto, off);
+        if (lane >= off) upto += v;
       }
-      rest -= __shfl_sync(0xffffffffu, pre, 31);
+      const int all = __shfl_sync(0xffffffffu, upto, 31);
+#pragma unroll 1
+      for (int k0 = 0; k0 < all; k0 += 32) {
+        const int k = k0 + lane;
+        int l = 0;   // the sequence of run k: as many as end at or before it
+#pragma unroll
+        for (int step = 16; step > 0; step >>= 1)
+          if (__shfl_sync(0xffffffffu, upto, l + step - 1) <= k) l += step;
+        l = imin(l, 31);
+        Seq o;
+        o.q0 = 0;
+        o.n = __shfl_sync(0xffffffffu, s.n, l);
+        o.len = __shfl_sync(0xffffffffu, s.len, l);
+        const int r = k - (__shfl_sync(0xffffffffu, upto, l) - __shfl_sync(0xffffffffu, runs, l));
+        int cost = 0;   // of one head
+        if (k < all) cost = tiles_of<BN>(g, o, r * g.tpi, imin(g.tpi, o.n - r * g.tpi)).count + g.item_cost;
+        if (pass == 0) {
+          sum += cost;
+          continue;
+        }
+        int pre = cost * g.Hk;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+          const int v = __shfl_up_sync(0xffffffffu, pre, off);
+          if (lane >= off) pre += v;
+        }
+        const unsigned hit = __ballot_sync(0xffffffffu, pre > rest);
+        if (hit) {
+          const int at = __ffs(hit) - 1;
+          const int one = imax(1, __shfl_sync(0xffffffffu, cost, at));
+          rest = imax(0, rest - (__shfl_sync(0xffffffffu, pre, at) - one * g.Hk));
+          p.b = b0 + __shfl_sync(0xffffffffu, l, at);
+          p.r = __shfl_sync(0xffffffffu, r, at);
+          p.h = imin(rest / one, g.Hk - 1);
+          p.t = imin(rest - p.h * one, one - 1);
+          return p;
+        }
+        rest -= __shfl_sync(0xffffffffu, pre, 31);
+      }
     }
-    break;
+    if (pass == 1) break;
+    p.W = imax(0, __reduce_add_sync(0xffffffffu, sum) * g.Hk);
+    p.shares = imin(p.W, ctas);
+    if (cta >= p.shares) return p;
+    rest = p.w0 = share_begin(p.W, cta, p.shares);
+    p.w1 = share_begin(p.W, cta + 1, p.shares);
   }
+  p.w1 = p.w0;   // not found: nothing to do
   return p;
 }
 
@@ -289,10 +252,10 @@ struct Walk {
     live = left > 0;
     if (!live) return false;
     c0 = 0;
-    if (++r == items_of(*g, s.n)) {
-      r = 0;
-      if (++h == g->Hk) {
-        h = 0;
+    if (++h == g->Hk) {
+      h = 0;
+      if (++r == items_of(*g, s.n)) {
+        r = 0;
         do {   // some is left, so a sequence with new tokens follows
           if (++b >= g->B) return live = false;
           s = load_seq(*g, b);
