@@ -186,8 +186,15 @@ def _call(index, fn, *args):
         return fn(*args)
 
 
-def _raw_stream(index, stream):
-    return torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+def _on(stream, fn, given):
+    """fn with the arguments `given` (their `stream` among them) and that stream
+    current: what the call allocates then belongs to the stream that uses it,
+    and is not handed out on another one while the kernels run."""
+    t = given["q"]
+    if t.is_cuda and stream.device != t.device:
+        raise ValueError(f"stream is on {stream.device}, q on {t.device}")
+    with torch.cuda.stream(stream):
+        return fn(**{**given, "stream": None})
 
 
 def _pack(pack, *fields):
@@ -290,6 +297,8 @@ def vda_qk_norm_rope(q, k, q_weight=None, k_weight=None, positions=None, frequen
     those places of k_cache and v_cache [pages, Hk, page_size, d] (slot = page
     * page_size + offset; -1: not stored).  Returns (q_out, k_out); k_out is
     None when only the cache receives k."""
+    if stream is not None:
+        return _on(stream, vda_qk_norm_rope, locals())
     N, Hq, Hk, d, dt = _qk_shapes(q, k)
     dtype, i = q.dtype, q.get_device()
     rows_q, rows_k, rows_v, rows_ko = _rows("q", q, dtype, (N, Hq, d), i), _rows("k", k, dtype, (N, Hk, d), i), (0, 0, 0), (0, 0, 0)
@@ -311,7 +320,7 @@ def vda_qk_norm_rope(q, k, q_weight=None, k_weight=None, positions=None, frequen
         pack_qk, dt, *rows_q, *rows_k, *rows_v, *_rows("q_out", q_out, dtype, (N, Hq, d), i), *rows_ko,
         _weight("q_weight", q_weight, d, i), _weight("k_weight", k_weight, d, i), pos, freq, ax,
         at_slots, at_kc, at_vc, N, Hq, Hk, d, axes, rot, 1 if interleaved else 0, pages, page, eps,
-        _raw_stream(i, stream))
+        torch._C._cuda_getCurrentRawStream(i))
     check(_call(i, lib().vda_qk_norm_rope, args), "vda_qk_norm_rope")
     return q_out, k_out
 
@@ -322,6 +331,8 @@ def vda_qk_norm_rope_backward(dq_out, dk_out, q, k, q_weight=None, k_weight=None
     [N, heads, d] (strided, or broadcast with stride 0, as they come) and its
     inputs, returns (dq, dk, dq_weight, dk_weight); the weight gradients are
     float32 [d], sums in a fixed order (None for a weight that is None)."""
+    if stream is not None:
+        return _on(stream, vda_qk_norm_rope_backward, locals())
     N, Hq, Hk, d, dt = _qk_shapes(q, k)
     dtype, i = q.dtype, q.get_device()
     pos, freq, ax, axes, rot = _rotation(N, positions, frequencies, axis, i)
@@ -343,7 +354,7 @@ def vda_qk_norm_rope_backward(dq_out, dk_out, q, k, q_weight=None, k_weight=None
         workspace = torch.empty(L.vda_qk_grad_workspace_bytes(d), dtype=torch.uint8, device=q.device)
     args = _pack(
         pack_qk_grad, dt, *rows, at_wq, at_wk, dwq.data_ptr() if at_wq else 0, dwk.data_ptr() if at_wk else 0, pos, freq, ax,
-        N, Hq, Hk, d, axes, rot, 1 if interleaved else 0, eps, _raw_stream(i, stream))
+        N, Hq, Hk, d, axes, rot, 1 if interleaved else 0, eps, torch._C._cuda_getCurrentRawStream(i))
     check(_call(i, L.vda_qk_norm_rope_backward, args, 0 if workspace is None else workspace.data_ptr(),
                 0 if workspace is None else workspace.numel()), "vda_qk_norm_rope_backward")
     return dq, dk, dwq, dwk
@@ -365,6 +376,8 @@ def vda_paged_attention(q, k_cache, v_cache, block_table, kv_len, q_start, block
     keys.  Returns out [N, Hq, d], or (out, lse [N, Hq] float32) with
     return_lse.  Calls that may overlap need workspaces of their own (the
     default is a new one)."""
+    if stream is not None:
+        return _on(stream, vda_paged_attention, locals())
     if q.dim() != 3:
         raise ValueError("q must be [N, Hq, d]")
     if not q.is_cuda:
@@ -406,7 +419,7 @@ def vda_paged_attention(q, k_cache, v_cache, block_table, kv_len, q_start, block
         pack_attn, dt, *rows_q, at_kc, at_vc, block_table.data_ptr(), _at("kv_len", kv_len, torch.int32, (B,), i),
         _at("q_start", q_start, torch.int32, (B + 1,), i), *_rows("out", out, dtype, (N, Hq, d), i), at_lse, table_stride,
         N, B, Hq, Hk, d, pages, page, max_pages, block, window_blocks, anchors, scale,
-        _raw_stream(i, stream))
+        torch._C._cuda_getCurrentRawStream(i))
     if workspace is None:
         n = _call(i, L.vda_paged_attention_workspace_bytes, dt, N, B, Hq, Hk, d, page)
         workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
