@@ -231,6 +231,15 @@ def _rows(name, t, dtype, shape, index):
     raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
 
 
+def _workspace(t, index):
+    """(address, bytes) of a workspace that the caller keeps, or of none."""
+    if t is None:
+        return 0, 0
+    if t.get_device() != index or not t.is_contiguous():
+        raise ValueError(f"workspace must be contiguous and on cuda:{index}")
+    return t.data_ptr(), t.numel() * t.element_size()
+
+
 def rope_frequencies(rot, theta=10000.0, sections=None, device="cuda"):
     """The (frequencies, axis) arguments of `vda_qk_norm_rope`: radians per
     position theta ** (-2 i / c) of the i-th pair of each axis, the c = 2 *
@@ -355,8 +364,7 @@ def vda_qk_norm_rope_backward(dq_out, dk_out, q, k, q_weight=None, k_weight=None
     args = _pack(
         pack_qk_grad, dt, *rows, at_wq, at_wk, dwq.data_ptr() if at_wq else 0, dwk.data_ptr() if at_wk else 0, pos, freq, ax,
         N, Hq, Hk, d, axes, rot, 1 if interleaved else 0, eps, torch._C._cuda_getCurrentRawStream(i))
-    check(_call(i, L.vda_qk_norm_rope_backward, args, 0 if workspace is None else workspace.data_ptr(),
-                0 if workspace is None else workspace.numel()), "vda_qk_norm_rope_backward")
+    check(_call(i, L.vda_qk_norm_rope_backward, args, *_workspace(workspace, i)), "vda_qk_norm_rope_backward")
     return dq, dk, dwq, dwk
 
 
@@ -423,7 +431,7 @@ def vda_paged_attention(q, k_cache, v_cache, block_table, kv_len, q_start, block
     if workspace is None:
         n = _call(i, L.vda_paged_attention_workspace_bytes, dt, N, B, Hq, Hk, d, page)
         workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
-    check(_call(i, L.vda_paged_attention, args, workspace.data_ptr(), workspace.numel()), "vda_paged_attention")
+    check(_call(i, L.vda_paged_attention, args, *_workspace(workspace, i)), "vda_paged_attention")
     return (out, lse) if return_lse else out
 
 

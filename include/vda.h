@@ -383,7 +383,8 @@ VDA_API int vda_qk_norm_rope_backward(const vda_qk_grad_args* args, void* worksp
  * at a key which one token sees can reach the other tokens of the sequence.
  * Query heads h with h / (Hq / Hk) equal share a KV head.  Tokens before
  * q_start[0] and from q_start[B] on are left as they were.
- * q, out, lse: rows as described above; lse [N, Hq] float32 contiguous or NULL.
+ * q, out, lse: rows as described above (on the tensor cores q is not a
+ * broadcast: its strides are at least 16 bytes); lse [N, Hq] float32 contiguous or NULL.
  * S, the softmax's maximum and sum and the output sums are float32; on the
  * tensor cores (bf16, d = 64 or 128, page_size a power of two from 8 on) the
  * weights are rounded to bf16 before their product with
