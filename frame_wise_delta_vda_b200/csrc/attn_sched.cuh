@@ -100,13 +100,24 @@ VDA_HD Tiles tiles_of(const Geom& g, const Seq& s, int i0, int ntok) {
   t.end = b.end;
   t.anc = b.anc;
   t.first = t.lo / BN;
-  t.n_anchor = imin((t.anc + BN - 1) / BN, t.first);
-  const int count = t.n_anchor + (t.end + BN - 1) / BN - t.first;
+  // unsigned: a length of up to 2^31 - 1 is rounded up past 31 bits
+  const auto upto = [](int k) { return (int)(((unsigned)k + BN - 1u) / BN); };
+  t.n_anchor = imin(upto(t.anc), t.first);
+  const int count = t.n_anchor + upto(t.end) - t.first;
   t.count = count > 1 ? count : 1;
   return t;
 }
 // key tile number of the item's tile t
 VDA_HD int key_tile(const Tiles& t, int i) { return i < t.n_anchor ? i : t.first + (i - t.n_anchor); }
+
+// Whether the n keys from j0 on lie all in [0, anc), or all in [lo, end); and
+// whether any of them lies in either.  j0 + n may pass 31 bits, so it is not formed.
+VDA_HD bool run_all_seen(int lo, int end, int anc, int j0, int n) {
+  return j0 <= anc - n || (j0 >= lo && j0 <= end - n);
+}
+VDA_HD bool run_any_seen(int lo, int end, int anc, int j0, int n) {
+  return j0 < anc || (j0 < end && j0 > lo - n);
+}
 
 // first tile of share g, and the share that holds tile x
 // (the first W % G shares have one tile more)

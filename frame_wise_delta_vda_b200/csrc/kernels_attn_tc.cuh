@@ -320,8 +320,9 @@ k_attn_tc(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUten
         // zeros: their coordinate lies outside the map.  -1: such a page,
         // -2: one that is seen but does not exist.
         auto page_row = [&](int t) -> int {
+          if (lane >= boxes) return -1;
           const int kt = t < n_anchor ? t : first + (t - n_anchor), j = kt * BN + lane * box;
-          if (lane >= boxes || !(j < anc || (j < end && j + box > lo))) return -1;
+          if (!run_any_seen(lo, end, anc, j, box)) return -1;
           const int id = __ldg(row_of + (j >> page_log2));
           return id >= 0 && id < cv.pages ? id * g.Hk + h : -2;
         };
@@ -330,7 +331,7 @@ k_attn_tc(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUten
           const int here = row;
           if (t + 1 < n) row = page_row(t0 + t + 1);
           const int kt = t0 + t < n_anchor ? t0 + t : first + (t0 + t - n_anchor);
-          const int off = (kt * BN + lane * box) & page_mask;
+          const int off = (int)(((uint32_t)kt * BN + (uint32_t)(lane * box)) & (uint32_t)page_mask);
           const uint32_t absent = __ballot_sync(0xffffffffu, here == -2);
 #pragma unroll
           for (int v = 0; v < 2; ++v) {
@@ -538,7 +539,7 @@ k_attn_tc(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUten
         tc_fence_after();
         // keys of the tile that no row of the item sees: their values may be
         // anything (0 x NaN would reach the sums), so they become zeros
-        if (!(j0 + BN <= it.anc || (j0 >= it.lo && j0 + BN <= it.end))) {
+        if (!run_all_seen(it.lo, it.end, it.anc, j0, BN)) {
           const uint32_t k = 2u * (base + (uint32_t)t) + 1u, s = k % C::NST;
           if (!wait(KVFULL + s, k / C::NST)) { ok = false; break; }
           const int j = j0 + r;
@@ -562,7 +563,7 @@ k_attn_tc(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUten
 #pragma unroll
         for (int c = 0; c < 4; ++c) tmem_ld32(tS + 32u * c, v[c]);
         const uint32_t absent = gone[(base + (uint32_t)t) % C::NGONE];   // pages of the tile that do not exist
-        const bool all = !valid || j0 + BN <= sp.anc || (j0 >= sp.lo && j0 + BN <= sp.end);
+        const bool all = !valid || run_all_seen(sp.lo, sp.end, sp.anc, j0, BN);
         const bool masked = !__all_sync(0xffffffffu, all && absent == 0u);
         tmem_wait_ld();
         if (masked) {
