@@ -19,6 +19,8 @@ _SCAN_FORMS = {"auto": VDA_SCAN_AUTO, "frames": VDA_SCAN_FRAMES, "chunks": VDA_S
 
 _DTYPES = {torch.bfloat16: VDA_BF16, torch.float32: VDA_F32}
 
+_F32_TINY = 2.0 ** -149   # the smallest positive float32
+
 
 def _ptr(t):
     return ctypes.c_void_p(t.data_ptr()) if t is not None else ctypes.c_void_p(0)
@@ -381,11 +383,15 @@ def vda_paged_attention(q, k_cache, v_cache, block_table, kv_len, q_start, block
     q_start[b] .. q_start[b + 1] and its last positions.  `block` 1 is causal
     by token, n >= 2 by blocks of n tokens, 0 sees every key; `window_blocks`
     blocks before a token's own are seen (-1: all) besides the first `anchors`
-    keys.  Returns out [N, Hq, d], or (out, lse [N, Hq] float32) with
-    return_lse.  Calls that may overlap need workspaces of their own (the
-    default is a new one)."""
+    keys.  `scale` defaults to 1 / sqrt(d).  Returns out [N, Hq, d], or
+    (out, lse [N, Hq] float32) with return_lse.  Calls that may overlap need
+    workspaces of their own (the default is a new one)."""
     if stream is not None:
         return _on(stream, vda_paged_attention, locals())
+    if scale is None:
+        scale = 0.0
+    elif not _F32_TINY <= scale < 1e30:   # what rounds to 0 would select the default
+        raise ValueError(f"scale must be at least 2 ** -149 and below 1e30, got {scale}")
     if q.dim() != 3:
         raise ValueError("q must be [N, Hq, d]")
     if not q.is_cuda:
@@ -418,10 +424,6 @@ def vda_paged_attention(q, k_cache, v_cache, block_table, kv_len, q_start, block
             at_lse = 0
     else:
         at_lse = _at("lse", lse, torch.float32, (N, Hq), i)
-    if scale is None:
-        scale = 0.0
-    elif not scale > 0.0:
-        raise ValueError(f"scale must be positive, got {scale}")
     L = lib()
     args = _pack(
         pack_attn, dt, *rows_q, at_kc, at_vc, block_table.data_ptr(), _at("kv_len", kv_len, torch.int32, (B,), i),
