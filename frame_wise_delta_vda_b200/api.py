@@ -19,7 +19,7 @@ _SCAN_FORMS = {"auto": VDA_SCAN_AUTO, "frames": VDA_SCAN_FRAMES, "chunks": VDA_S
 
 _DTYPES = {torch.bfloat16: VDA_BF16, torch.float32: VDA_F32}
 
-_F32_TINY = 2.0 ** -149   # the smallest positive float32
+_F32_TINY, _F32_MAX = 2.0 ** -149, (2.0 - 2.0 ** -23) * 2.0 ** 127   # the positive float32's
 
 
 def _ptr(t):
@@ -277,7 +277,9 @@ def _weight(name, w, d, index):
     return 0 if w is None else _at(name, w, torch.float32, (d,), index)
 
 
-def _qk_shapes(q, k):
+def _qk_shapes(q, k, eps):
+    if not _F32_TINY <= eps <= _F32_MAX:   # what rounds to 0 would select the default
+        raise ValueError(f"eps must be a positive float32, got {eps}")
     if q.dim() != 3 or k.dim() != 3:
         raise ValueError("q and k must be [N, heads, d]")
     if not q.is_cuda:
@@ -302,15 +304,15 @@ def vda_qk_norm_rope(q, k, q_weight=None, k_weight=None, positions=None, frequen
                      k_out=None, stream=None):
     """RMS norm of each head of q [N, Hq, d] and k [N, Hk, d] (weights [d]
     float32) and the rotation of its first 2 * len(frequencies) channels by
-    positions [N, axes] int32 (see include/vda.h and `rope_frequencies`).
-    q, k and v may be strided over tokens and heads (slices of a joint
+    positions [N, axes] int32 (see include/vda.h and `rope_frequencies`);
+    `eps` is positive.  q, k and v may be strided over tokens and heads (slices of a joint
     projection).  With `slots` [N] int64, k's result and v [N, Hk, d] go to
     those places of k_cache and v_cache [pages, Hk, page_size, d] (slot = page
     * page_size + offset; -1: not stored).  Returns (q_out, k_out); k_out is
     None when only the cache receives k."""
     if stream is not None:
         return _on(stream, vda_qk_norm_rope, locals())
-    N, Hq, Hk, d, dt = _qk_shapes(q, k)
+    N, Hq, Hk, d, dt = _qk_shapes(q, k, eps)
     dtype, i = q.dtype, q.get_device()
     rows_q, rows_k, rows_v, rows_ko = _rows("q", q, dtype, (N, Hq, d), i), _rows("k", k, dtype, (N, Hk, d), i), (0, 0, 0), (0, 0, 0)
     pos, freq, ax, axes, rot = _rotation(N, positions, frequencies, axis, i)
@@ -344,7 +346,7 @@ def vda_qk_norm_rope_backward(dq_out, dk_out, q, k, q_weight=None, k_weight=None
     float32 [d], sums in a fixed order (None for a weight that is None)."""
     if stream is not None:
         return _on(stream, vda_qk_norm_rope_backward, locals())
-    N, Hq, Hk, d, dt = _qk_shapes(q, k)
+    N, Hq, Hk, d, dt = _qk_shapes(q, k, eps)
     dtype, i = q.dtype, q.get_device()
     pos, freq, ax, axes, rot = _rotation(N, positions, frequencies, axis, i)
     if dq is None:

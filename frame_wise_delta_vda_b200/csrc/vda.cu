@@ -454,8 +454,9 @@ bool rows_out_ok(const vda_rows& r, int64_t N, int64_t heads, int64_t d, size_t 
 }
 
 int check_qk_sizes(int dtype, int N, int Hq, int Hk, int d, int axes, int rot, const int* positions,
-                   const double* frequencies, const int* axis) {
+                   const double* frequencies, const int* axis, float eps) {
   if (dtype != VDA_BF16 && dtype != VDA_F32) return VDA_ERR_INVALID_ARGUMENT;
+  if (!std::isfinite(eps)) return VDA_ERR_INVALID_ARGUMENT;
   if (N < 0 || Hq < 1 || Hk < 1 || d < 1 || rot < 0 || rot > d) return VDA_ERR_INVALID_ARGUMENT;
   if (d != 16 && d != 32 && d != 64 && d != 128) return VDA_ERR_UNSUPPORTED;
   if (rot % 16 != 0 || Hq > 65536 || Hk > 65536) return VDA_ERR_UNSUPPORTED;
@@ -558,7 +559,7 @@ int vda_paged_attention(const vda_attn_args* a, void* workspace, size_t workspac
 int vda_qk_norm_rope(const vda_qk_args* a) {
   if (!a) return VDA_ERR_INVALID_ARGUMENT;
   const int rc = check_qk_sizes(a->dtype, a->N, a->Hq, a->Hk, a->d, a->axes, a->rot, a->positions, a->frequencies,
-                                a->axis);
+                                a->axis, a->eps);
   if (rc != VDA_OK) return rc;
   if (!aligned4(a->q_weight) || !aligned4(a->k_weight)) return VDA_ERR_INVALID_ARGUMENT;
   if (a->slots) {
@@ -587,7 +588,7 @@ size_t vda_qk_grad_workspace_bytes(int d) {
 int vda_qk_norm_rope_backward(const vda_qk_grad_args* a, void* workspace, size_t workspace_bytes) {
   if (!a) return VDA_ERR_INVALID_ARGUMENT;
   const int rc = check_qk_sizes(a->dtype, a->N, a->Hq, a->Hk, a->d, a->axes, a->rot, a->positions, a->frequencies,
-                                a->axis);
+                                a->axis, a->eps);
   if (rc != VDA_OK) return rc;
   if (!aligned4(a->q_weight) || !aligned4(a->k_weight) || !aligned4(a->dq_weight) || !aligned4(a->dk_weight))
     return VDA_ERR_INVALID_ARGUMENT;

@@ -324,7 +324,7 @@ typedef struct vda_qk_args {
   int N, Hq, Hk, d;
   int axes, rot, interleaved;
   int pages, page_size;       /* >= 1 when slots is set */
-  float eps;                  /* <= 0 selects 1e-6 */
+  float eps;                  /* finite; <= 0 selects 1e-6 */
   void* stream;               /* cudaStream_t */
 } vda_qk_args;
 
@@ -356,7 +356,7 @@ typedef struct vda_qk_grad_args {
   const int* axis;
   int N, Hq, Hk, d;
   int axes, rot, interleaved;
-  float eps;
+  float eps;                  /* as in vda_qk_args */
   void* stream;
 } vda_qk_grad_args;
 
