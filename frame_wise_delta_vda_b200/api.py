@@ -202,7 +202,7 @@ def _on(stream, fn, given):
 def _pack(pack, *fields):
     try:
         return pack(*fields)
-    except (struct.error, OverflowError) as e:   # a number that its C type does not hold
+    except struct.error as e:   # a size that its C type does not hold
         raise ValueError(f"argument out of range: {e}") from None
 
 
