@@ -128,20 +128,29 @@ __device__ __forceinline__ Place place_of(int lane, int c0, int rot) {
 }
 
 // cos and sin of one pair's angle.  It is held in turns as a 64-bit binary
-// fraction: the frequency is brought to one (53 significant bits), and its
-// product with the integer position wraps without rounding, so a far position
-// keeps its angle (to position * 2^-55 turns) where a 32-bit product of
-// radians loses it.
+// fraction: the frequency is brought to one, and its product with the integer
+// position wraps without rounding, so a far position keeps its angle where a
+// 32-bit product of radians loses it.  1 / (2 pi) comes in two parts and the
+// product's rounding error is kept, as the whole turns of a frequency above one
+// radian would take the digits behind them: the step is off by at most 2^-64
+// turns (|frequency| <= 2^40; with one part it was 2^-49 turns at 100 radians).
+// The phase is then rounded to the 24 bits of a float, 2^-25 turns with what is
+// cut before; fp32 functions of it are off by 2^-23, and more bits of their
+// argument would not show in a result of 24.
 __device__ __forceinline__ void pair_angle(const Turn& t, int64_t token, int pair, float& c, float& s) {
   c = 1.f;
   s = 0.f;
   const int ax = __ldg(t.axis + pair);
   if (ax < 0 || ax >= t.axes) return;
-  double turns = __ldg(t.freq + pair) * 0.15915494309189533577;
-  turns -= floor(turns);
-  const unsigned long long step = __double2ull_rn(turns * 18446744073709551616.0);
+  constexpr double kHi = 0.15915494309189535, kLo = -9.839338337591243e-18;   // 1 / (2 pi)
+  const double f = __ldg(t.freq + pair), turns = f * kHi;
+  double rest = fma(f, kLo, fma(f, kHi, -turns));   // what the product lost
+  rest -= rint(rest);
+  constexpr double kTurn = 18446744073709551616.0;
+  const unsigned long long step = (unsigned long long)__double2ll_rn((turns - rint(turns)) * kTurn) +
+                                  (unsigned long long)__double2ll_rn(rest * kTurn);
   const long long pos = __ldg(t.pos + token * t.axes + ax);
-  const int frac = (int)(((unsigned long long)pos * step) >> 32);   // signed: half a turn either way
+  const int frac = (int)(((unsigned long long)pos * step + 0x80000000ull) >> 32);   // signed: half a turn either way
   sincospif((float)frac * 4.656612873077392578125e-10f, &s, &c);
 }
 

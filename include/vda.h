@@ -298,8 +298,9 @@ typedef struct vda_rows {
  * R turns pair p of the first rot channels by position[axis[p]] * frequencies[p]:
  *   (y_i, y_j) = (z_i cos - z_j sin, z_j cos + z_i sin),
  *   (i, j) = (p, p + rot / 2), or (2 p, 2 p + 1) when interleaved.
- * Sums and angles are held in 32 bits or more; the phase of an integer
- * position is exact to position * 2^-55 turns.  y is rounded once.
+ * Sums are held in 32 bits or more; the phase of an integer position is off
+ * by at most 2^-25 + |position| 2^-64 turns for frequencies of either sign up
+ * to 2^40.  y is rounded once.
  * With slots set, k's y and v (unchanged) also go to place slots[token] =
  * page * page_size + offset of the paged cache [pages, Hk, page_size, d]; a
  * token whose slot lies outside [0, pages * page_size) is not stored (give -1
