@@ -494,7 +494,8 @@ int dispatch_qk_bwd(const vda_qk_grad_args& a, float* part, float eps, int sms) 
 
 int check_attn_sizes(int dtype, int N, int B, int Hq, int Hk, int d, int page) {
   if (dtype != VDA_BF16 && dtype != VDA_F32) return VDA_ERR_INVALID_ARGUMENT;
-  if (N < 0 || B < 1 || Hq < 1 || Hk < 1 || d < 1 || page < 1 || Hq % Hk != 0) return VDA_ERR_INVALID_ARGUMENT;
+  // a batch of no sequences has no tokens
+  if (N < 0 || B < (N > 0 ? 1 : 0) || Hq < 1 || Hk < 1 || d < 1 || page < 1 || Hq % Hk != 0) return VDA_ERR_INVALID_ARGUMENT;
   if (d != 16 && d != 32 && d != 64 && d != 128) return VDA_ERR_UNSUPPORTED;
   const int G = Hq / Hk;
   if (!vda::attn::tc_supported(dtype, d, G, page) && G > 64) return VDA_ERR_UNSUPPORTED;
@@ -524,17 +525,17 @@ int vda_paged_attention(const vda_attn_args* a, void* workspace, size_t workspac
   if (!a) return VDA_ERR_INVALID_ARGUMENT;
   const int rc = check_attn_sizes(a->dtype, a->N, a->B, a->Hq, a->Hk, a->d, a->page_size);
   if (rc != VDA_OK) return rc;
-  if (a->pages < 1 || a->max_pages < 1 || a->table_stride < 0 || a->block < 0 || a->anchors < 0 ||
+  if (a->pages < 1 || a->max_pages < (a->N > 0 ? 1 : 0) || a->table_stride < 0 || a->block < 0 || a->anchors < 0 ||
       !(a->scale >= 0.f && a->scale < 1e30f))
     return VDA_ERR_INVALID_ARGUMENT;
   if (a->block > (1 << 30) || a->anchors > (1 << 30) || (double)a->pages * a->Hk > 2147483647.0 ||
       (double)a->pages * a->Hk * a->page_size * a->d > 4.0e15)
     return VDA_ERR_UNSUPPORTED;
   if (!a->k_cache || !a->v_cache || !aligned16(a->k_cache) || !aligned16(a->v_cache)) return VDA_ERR_INVALID_ARGUMENT;
+  if (a->N == 0) return VDA_OK;
   if (!a->block_table || !a->kv_len || !a->q_start || !aligned4(a->block_table) || !aligned4(a->kv_len) ||
       !aligned4(a->q_start) || !aligned4(a->lse))
     return VDA_ERR_INVALID_ARGUMENT;
-  if (a->N == 0) return VDA_OK;
   const size_t es = elem_size(a->dtype);
   if (!rows_ok(a->q, a->N, a->Hq, es) || !rows_out_ok(a->out, a->N, a->Hq, a->d, es)) return VDA_ERR_INVALID_ARGUMENT;
   const vda::attn::AttnPlan p =

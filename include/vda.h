@@ -392,7 +392,8 @@ VDA_API int vda_qk_norm_rope_backward(const vda_qk_grad_args* args, void* worksp
  * V, their sum is not.  Other types and sizes run on a SIMT kernel in float32.
  * Supported: d in {16, 32, 64, 128}; Hq / Hk up to 128 on the tensor cores,
  * 64 elsewhere; pages * Hk < 2^31.  The lengths and the table are read on the
- * device: a captured call follows them.  N = 0 is a valid empty call.
+ * device: a captured call follows them.  N = 0 is a valid empty call, with B
+ * and max_pages from 0 on and without the arrays of sequences.
  * Workspace: vda_paged_attention_workspace_bytes(), device, 256-byte aligned;
  * calls that may overlap need one each.  Returns vda_status. */
 typedef struct vda_attn_args {
