@@ -305,11 +305,12 @@ def vda_qk_norm_rope(q, k, q_weight=None, k_weight=None, positions=None, frequen
     """RMS norm of each head of q [N, Hq, d] and k [N, Hk, d] (weights [d]
     float32) and the rotation of its first 2 * len(frequencies) channels by
     positions [N, axes] int32 (see include/vda.h and `rope_frequencies`);
-    `eps` is positive.  q, k and v may be strided over tokens and heads (slices of a joint
-    projection).  With `slots` [N] int64, k's result and v [N, Hk, d] go to
-    those places of k_cache and v_cache [pages, Hk, page_size, d] (slot = page
-    * page_size + offset; -1: not stored).  Returns (q_out, k_out); k_out is
-    None when only the cache receives k."""
+    `eps` is positive.  q, k and v may be strided over tokens and heads (slices
+    of a joint projection).  With `slots` [N] int64, k's result and v [N, Hk, d]
+    go to those places of k_cache and v_cache [pages, Hk, page_size, d] (slot =
+    page * page_size + offset; -1: not stored).  Results must not lie on inputs
+    (not in place).  Returns (q_out, k_out); k_out is None when only the cache
+    receives k."""
     if stream is not None:
         return _on(stream, vda_qk_norm_rope, locals())
     N, Hq, Hk, d, dt = _qk_shapes(q, k, eps)

@@ -13,6 +13,7 @@
 #include <cmath>
 #include <cstdio>
 #include <cstring>
+#include <initializer_list>
 #include <mutex>
 #include <vector>
 
@@ -23,6 +24,7 @@
 #include "kernels_prep.cuh"
 #include "kernels_qk.cuh"
 #include "kernels_attn_tc.cuh"
+#include "overlap.cuh"
 
 namespace {
 
@@ -453,6 +455,28 @@ bool rows_out_ok(const vda_rows& r, int64_t N, int64_t heads, int64_t d, size_t 
   return nested(r.head_stride, heads, r.token_stride, N) || nested(r.token_stride, N, r.head_stride, heads);
 }
 
+vda::Region region(const vda_rows& r, int64_t N, int64_t heads, int64_t d, size_t es) {
+  if (!r.data) return vda::make_region(nullptr, 0);
+  const int64_t e = (int64_t)es;
+  return vda::make_region(r.data, d * e, N, N > 1 ? r.token_stride * e : 0, heads, heads > 1 ? r.head_stride * e : 0);
+}
+// n contiguous values, or nothing
+template <typename T>
+vda::Region region(const T* p, int64_t n) {
+  return vda::make_region(p, p ? n * (int64_t)sizeof(T) : 0);
+}
+// Results lie apart from what is read and from one another: kernels read
+// through the read-only path, and no order between rows is kept.
+bool apart(std::initializer_list<vda::Region> results, std::initializer_list<vda::Region> inputs) {
+  for (const vda::Region* r = results.begin(); r != results.end(); ++r) {
+    for (const vda::Region* o = r + 1; o != results.end(); ++o)
+      if (vda::overlap(*r, *o)) return false;
+    for (const vda::Region& i : inputs)
+      if (vda::overlap(*r, i)) return false;
+  }
+  return true;
+}
+
 int check_qk_sizes(int dtype, int N, int Hq, int Hk, int d, int axes, int rot, const int* positions,
                    const double* frequencies, const int* axis, float eps) {
   if (dtype != VDA_BF16 && dtype != VDA_F32) return VDA_ERR_INVALID_ARGUMENT;
@@ -550,6 +574,13 @@ int vda_paged_attention(const vda_attn_args* a, void* workspace, size_t workspac
   if (!workspace || (reinterpret_cast<uintptr_t>(workspace) % kAlign) != 0 || workspace_bytes < p.total)
     return VDA_ERR_WORKSPACE;
   char* ws = static_cast<char*>(workspace);
+  const int64_t cache = (int64_t)a->pages * a->Hk * a->page_size * a->d * (int64_t)es;
+  if (!apart({region(a->out, a->N, a->Hq, a->d, es), region(a->lse, (int64_t)a->N * a->Hq), region(ws, (int64_t)p.total)},
+             {region(a->q, a->N, a->Hq, a->d, es), region(static_cast<const char*>(a->k_cache), cache),
+              region(static_cast<const char*>(a->v_cache), cache),
+              region(a->block_table, (a->B - 1) * a->table_stride + a->max_pages), region(a->kv_len, a->B),
+              region(a->q_start, a->B + 1LL)}))
+    return VDA_ERR_INVALID_ARGUMENT;
   // exponents in base 2
   const float scale = a->scale > 0.f ? a->scale : 1.f / sqrtf((float)a->d);
   const float c2 = scale * vda::attn::kLog2e;
@@ -576,6 +607,15 @@ int vda_qk_norm_rope(const vda_qk_args* a) {
     return VDA_ERR_INVALID_ARGUMENT;
   if ((!a->slots || a->k_out.data) && !rows_out_ok(a->k_out, a->N, a->Hk, a->d, es)) return VDA_ERR_INVALID_ARGUMENT;
   if (a->slots && !rows_ok(a->v_in, a->N, a->Hk, es)) return VDA_ERR_INVALID_ARGUMENT;
+  const int64_t cache = a->slots ? (int64_t)a->pages * a->Hk * a->page_size * a->d * (int64_t)es : 0;
+  const int64_t half = a->rot / 2;
+  if (!apart({region(a->q_out, a->N, a->Hq, a->d, es), region(a->k_out, a->N, a->Hk, a->d, es),
+              region(static_cast<const char*>(a->k_cache), cache), region(static_cast<const char*>(a->v_cache), cache)},
+             {region(a->q_in, a->N, a->Hq, a->d, es), region(a->k_in, a->N, a->Hk, a->d, es),
+              region(a->slots ? a->v_in : vda_rows{}, a->N, a->Hk, a->d, es), region(a->q_weight, a->d),
+              region(a->k_weight, a->d), region(a->positions, half > 0 ? (int64_t)a->N * a->axes : 0),
+              region(a->frequencies, half), region(a->axis, half), region(a->slots, a->N)}))
+    return VDA_ERR_INVALID_ARGUMENT;
   const float eps = a->eps > 0.f ? a->eps : 1e-6f;
   const int sms = vda::tc::num_sms();
   return a->dtype == VDA_BF16 ? dispatch_qk_fwd<__nv_bfloat16>(*a, eps, sms) : dispatch_qk_fwd<float>(*a, eps, sms);
@@ -608,6 +648,15 @@ int vda_qk_norm_rope_backward(const vda_qk_grad_args* a, void* workspace, size_t
   if (sums && (!workspace || (reinterpret_cast<uintptr_t>(workspace) % kAlign) != 0 ||
                workspace_bytes < vda_qk_grad_workspace_bytes(a->d)))
     return VDA_ERR_WORKSPACE;
+  const int64_t half = a->rot / 2;
+  if (!apart({region(a->dq_in, a->N, a->Hq, a->d, es), region(a->dk_in, a->N, a->Hk, a->d, es), region(a->dq_weight, a->d),
+              region(a->dk_weight, a->d),
+              region(static_cast<const char*>(workspace), sums ? (int64_t)vda_qk_grad_workspace_bytes(a->d) : 0)},
+             {region(a->dq_out, a->N, a->Hq, a->d, es), region(a->dk_out, a->N, a->Hk, a->d, es),
+              region(a->q_in, a->N, a->Hq, a->d, es), region(a->k_in, a->N, a->Hk, a->d, es), region(a->q_weight, a->d),
+              region(a->k_weight, a->d), region(a->positions, half > 0 ? (int64_t)a->N * a->axes : 0),
+              region(a->frequencies, half), region(a->axis, half)}))
+    return VDA_ERR_INVALID_ARGUMENT;
   const float eps = a->eps > 0.f ? a->eps : 1e-6f;
   const int sms = vda::tc::num_sms();
   float* part = sums ? static_cast<float*>(workspace) : nullptr;

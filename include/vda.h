@@ -286,7 +286,9 @@ VDA_API int vda_prep(const vda_prep_args* args);
  * multiples of 16 bytes, so slices of a joint [q | k | v] projection and
  * head-major tensors are taken as they are.  Inputs may have stride 0
  * (broadcast); rows of outputs must not overlap, neither one another nor an
- * input. */
+ * input: there is no form in place.  Such a call is refused where the larger
+ * strides of the two are alike, as those of views of one tensor are, or one is
+ * contiguous; other overlaps are not looked for. */
 typedef struct vda_rows {
   void* data;
   int64_t token_stride;
