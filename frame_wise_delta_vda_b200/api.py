@@ -385,8 +385,9 @@ def vda_paged_attention(q, k_cache, v_cache, block_table, kv_len, q_start, block
     q_start [B + 1] are int32 on the device; sequence b's new tokens are rows
     q_start[b] .. q_start[b + 1] and its last positions.  `block` 1 is causal
     by token, n >= 2 by blocks of n tokens, 0 sees every key; `window_blocks`
-    blocks before a token's own are seen (-1: all) besides the first `anchors`
-    keys.  `scale` defaults to 1 / sqrt(d).  Returns out [N, Hq, d], or
+    blocks before a token's own are seen (-1: all), and those of the first
+    `anchors` keys that lie before the end of its own block; blocks are counted
+    from the end of the anchors.  `scale` defaults to 1 / sqrt(d).  Returns out [N, Hq, d], or
     (out, lse [N, Hq] float32) with return_lse.  Calls that may overlap need
     workspaces of their own (the default is a new one)."""
     if stream is not None:

@@ -45,7 +45,8 @@ struct Geom {
 VDA_HD int imin(int a, int b) { return a < b ? a : b; }
 VDA_HD int imax(int a, int b) { return a > b ? a : b; }
 
-// keys seen from position p of a sequence of len keys
+// Keys seen from position p of a sequence of len keys.  Anchors behind the end
+// of the token's own block are not seen.
 VDA_HD Span span_of(const Geom& g, int p, int len) {
   Span s;
   if (p < 0) {

@@ -377,8 +377,10 @@ VDA_API int vda_qk_norm_rope_backward(const vda_qk_grad_args* args, void* worksp
  *   block >= 1: positions fall into blocks floor((p - anchors) / block); the
  *               token sees its own block whole (block = 1: causal by token,
  *               block = tokens of a chunk: causal by chunk), the window_blocks
- *               blocks before it (< 0: every block before it) and the first
- *               `anchors` keys.
+ *               blocks before it (< 0: every block before it) and, of the first
+ *               `anchors` keys, those before the end of its own block.  Anchors
+ *               are keys that came first: a token among them, or in a block
+ *               that ends among them, does not see the later ones.
  * A token that sees nothing (p < 0, or no key) gets o = 0 and lse = -inf.  A
  * key whose page id lies outside [0, pages) is not seen, whatever mask holds
  * (an evicted page).  What lies in the cache at places that no new token of
