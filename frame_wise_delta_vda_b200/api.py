@@ -387,7 +387,9 @@ def vda_paged_attention(q, k_cache, v_cache, block_table, kv_len, q_start, block
     by token, n >= 2 by blocks of n tokens, 0 sees every key; `window_blocks`
     blocks before a token's own are seen (-1: all), and those of the first
     `anchors` keys that lie before the end of its own block; blocks are counted
-    from the end of the anchors.  `scale` defaults to 1 / sqrt(d).  Returns out [N, Hq, d], or
+    from the end of the anchors.  Other sets of keys, such as a window on both
+    sides of a clip's chunk, are given by the table: a sequence per chunk with
+    block 0, whose row lists the (shared, full) pages it sees.  `scale` defaults to 1 / sqrt(d).  Returns out [N, Hq, d], or
     (out, lse [N, Hq] float32) with return_lse.  Calls that may overlap need
     workspaces of their own (the default is a new one)."""
     if stream is not None:

@@ -381,6 +381,10 @@ VDA_API int vda_qk_norm_rope_backward(const vda_qk_grad_args* args, void* worksp
  *               `anchors` keys, those before the end of its own block.  Anchors
  *               are keys that came first: a token among them, or in a block
  *               that ends among them, does not see the later ones.
+ * Keys that are no such run, as those of a clip's chunk (the chunks on both
+ * sides of it, the anchor frames at both ends): give each chunk as a sequence
+ * with block = 0 whose row of the block table lists the pages of what it
+ * sees.  Rows may share pages; all but the last page of a row must be full.
  * A token that sees nothing (p < 0, or no key) gets o = 0 and lse = -inf.  A
  * key whose page id lies outside [0, pages) is not seen, whatever mask holds
  * (an evicted page).  What lies in the cache at places that no new token of
