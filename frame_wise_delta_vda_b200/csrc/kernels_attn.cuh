@@ -68,10 +68,12 @@ __device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
 // ===========================================================================
 // k_attn_simt: float32 I/O and head sizes without a tensor-core kernel.
 // BM rows x 64 keys a tile; thread (ty, tx) of 16 x 16 has BM / 16 rows x 4 keys
-// of the scores and BM / 16 rows x D / 16 channels of the output.  Bound by the
-// fp32 FMA pipe: the register tiles read two to three 16-B words of shared
-// memory per 32 FMAs.  fp32, 4 x 256 tokens over 2000 keys, 8 / 2 heads of 64:
-// 159 us (24 TFLOP/s).
+// of the scores and BM / 16 rows x D / 16 channels of the output.  Bound by
+// shared memory, not by the FMA pipe: at BM = 64 and D = 64 a thread reads eight
+// 16-B words for 64 FMAs in the scores and again in P V, at BM = 16 five for 16.
+// fp32, 4 x 256 tokens over 2000 keys, 8 / 2 heads: 160 us at d = 64 (24.6
+// TFLOP/s of the pipe's 74) and 361 us at d = 128 (21.8), where 117 KB of shared
+// memory let one CTA of the two per SM that the plan makes run at a time.
 // ===========================================================================
 template <int D, int BM>
 struct SimtCfg {
@@ -333,8 +335,11 @@ k_attn_join(Parts parts, OutView<T> ov, int group) {
 inline size_t align256(size_t x) { return (x + 255) / 256 * 256; }
 
 // What an item costs besides its key tiles, in tiles (Q's load, the first
-// scores, the output).  64 single tokens over 246 to 8200 keys: the last CTA
-// ended at 163 us with 0, at 135 with 3.
+// scores, the output).  32 / 8 heads of 128, with 0, 1, 3 and 6 in us: 64 single
+// tokens over 246 to 8200 keys 176, 168, 150, 154; 200 over 100 to 600 keys 184,
+// 168, 164, 166; 17 over 500 to 30000 keys 145, 135, 126, 127; 40 sequences of 1
+// to 5 tokens over 50 to 3000 keys 96, 92, 88, 88; 6 prompts of 30 to 900 tokens
+// over 900 to 4000 keys 133, 129, 121, 123.
 constexpr int kTcItemCost = 3;
 
 struct AttnPlan {

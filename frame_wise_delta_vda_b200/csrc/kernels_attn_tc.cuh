@@ -15,11 +15,24 @@
 // outgrows it by 2^8 (P stays in bf16's range and the quotient is the same),
 // so the output in TMEM is rarely scaled.
 //
-// Measured, 32 / 8 heads of 128: 4096 tokens over 16400 keys 1024 us (57% of
-// the measured bf16 rate), bound by the chain of a turn (scores, maximum,
+// P is rounded to bf16 (its sum l is not): both operands of a product have one
+// type, and V is bf16.  A weight is off by at most 2^-8 of itself, so the result
+// by at most that of sum_j p_j |v_j|; measured against 64 bits, 2.1e-3 to 2.3e-3
+// of the result's norm, where rounding the result alone gives 1.7e-3.  P as two
+// bf16 terms would take the difference away, for twice the products of P V.
+//
+// Measured, 32 / 8 heads of 128: 4096 tokens over 16400 keys 1004 to 1017 us (58%
+// of the measured bf16 rate), bound by the chain of a turn (scores, maximum,
 // exponentials, product: 2285 cycles a tile, 1024 of either pipe); 64 steps over
-// 246 to 8200 keys 156 us (69% of a plain copy's rate) and 2 over 131000 keys
-// 192 us (85%), bound by memory and by the items' begin and end.
+// 246 to 8200 keys 154 to 157 us (70% of a plain copy's rate) and 2 over 131000
+// keys 189 to 193 us (85%), bound by memory and by the items' begin and end.
+// 4096 tokens over 16400 keys with 32 / 8 heads of 64: 826 us (583 TFLOP/s), the
+// same chain for half the products.
+//
+// Registers: three values that are set once at the start live in local memory
+// (12 bytes stored) and are read again at some 150 places (624 bytes of reloads
+// in the code), more than half of them in the loops of waits that go on: with
+// those compiled out 296 bytes are left.
 //
 // Warps 0-3 and 4-7: softmax and output of turn 0 and 1; warp 8: K, V loads;
 // warps 9 and 10: MMA of turn 0 and 1; warp 11: the list of items and Q loads.

@@ -18,10 +18,10 @@
 // (bf16 pairs): with 157 instructions for two rows instead of 113 the
 // kernel was bound by issue.
 //
-// Measured, bf16, 60480 tokens of 48 + 48 heads of 128, three axes: 555 us with
-// 80 registers and 6 blocks an SM (2.97 GB, 82% of a plain copy's rate; 778 us
-// with 157 instructions).  The gradient, 20160 such tokens: 303 us with 128
-// registers and 4 blocks an SM (1.49 GB, 74%).  Both then wait for memory
+// Measured, bf16, 60480 tokens of 48 + 48 heads of 128, three axes: 542 to 562 us
+// with 80 registers and 6 blocks an SM (2.97 GB, 81 to 84% of a plain copy's rate;
+// 778 us with 157 instructions).  The gradient, 20160 such tokens: 302 us with 128
+// registers and 4 blocks an SM (1.49 GB, 75%).  Both then wait for memory
 // with the warps that their registers allow.
 #pragma once
 
@@ -270,7 +270,9 @@ k_qk_norm_rope(const __grid_constant__ FwdArgs<T> a) {
   // rows [h0, h1) of q or of k
   auto heads = [&](bool isq, int h0, int h1) {
     const float* w = isq ? a.wq : a.wk;
-    float2 wc[4], ws[4];   // weight times cos, the paired channel's weight times sin
+    // weight times cos, the paired channel's weight times sin: once a token instead
+    // of once a row, for one more rounding of 2^-24
+    float2 wc[4], ws[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const float2 wi = weight2(w, c0 + 2 * i), wp = weight2(w, pl.pc0 + 2 * i);
