@@ -310,7 +310,8 @@ def vda_qk_norm_rope(q, k, q_weight=None, k_weight=None, positions=None, frequen
     go to those places of k_cache and v_cache [pages, Hk, page_size, d] (slot =
     page * page_size + offset; -1: not stored).  Results must not lie on inputs
     (not in place).  Returns (q_out, k_out); k_out is None when only the cache
-    receives k."""
+    receives k.  Autograd does not see the call: its gradient is
+    `vda_qk_norm_rope_backward`."""
     if stream is not None:
         return _on(stream, vda_qk_norm_rope, locals())
     N, Hq, Hk, d, dt = _qk_shapes(q, k, eps)
